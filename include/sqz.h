@@ -371,6 +371,89 @@ SQZ_API sqz_status sqz_encode(const uint16_t* w, int32_t n_out, int32_t k_in, in
  * (2*m above; 0 for n_weights <= 0 or a negative or NaN fraction). */
 SQZ_API int64_t sqz_encode_outliers(int64_t n_weights, double outlier_fraction);
 
+/* ------------------------------------- 8-bit floating point, block scales ---
+ * Products whose operands are 8-bit floating-point codes with one fp32 scale
+ * for each block of 128 columns (of K), for calls the LUT kernels do not
+ * serve: more than SQZ_MAX_BATCH columns (prompts; sqz_debug_dequant followed
+ * by sqz_fp8_quantize turns a layer's dense part into such a matrix) and
+ * layers kept at 8 bits.
+ *
+ * A matrix X [rows][k] is held as codes q [rows][ld] (row-major, bytes) and
+ * scales [ceil(rows / block_rows)][ld_scale]: X(r,c) = scale(r / block_rows,
+ * c / 128) * value(q(r,c)), block_rows = 1 for activations and 128 for
+ * weights.  The last block of a row or column may be partial.  Codes start on
+ * a 16-byte boundary and ld is a multiple of 16 (the copy engine's rule);
+ * bytes between column k and ld are never read or written.
+ */
+#define SQZ_FP8_E4M3 0 /* 1-4-3, largest finite value 448, no infinity   */
+#define SQZ_FP8_E5M2 1 /* 1-5-2, largest finite value 57344              */
+
+#define SQZ_TYPE_F16 0
+#define SQZ_TYPE_BF16 1
+#define SQZ_TYPE_F32 2
+
+/*
+ * Quantize `batch` matrices x [rows][ldx] (fp16 or bf16, stored one after the
+ * other) to codes q [batch * rows][ldq] and scales
+ * [batch * ceil(rows / block_rows)][ld_scale].  Definition (exact, so the
+ * result is unique): per block, scale = max|x| / F in fp32 (F = 448 or 57344;
+ * scale 1 for a block of zeros), code = x / scale in fp32, rounded to the
+ * nearest code (ties to even), quotients beyond F giving F.  A block with a
+ * NaN has a NaN scale and NaN codes; one with an infinity (and no NaN) has an
+ * infinite scale, NaN codes at the infinities and 0 elsewhere.  Any alignment
+ * of x and any ldx >= cols is taken (rows on 16-byte boundaries are faster).
+ * Asynchronous on `stream`; x, q and scale must not overlap.
+ *
+ * Errors: SQZ_ERR_INVALID_ARG for an unknown x_type (fp16 or bf16), format or
+ * block_rows (1 or 128), negative sizes, NULL arrays of a non-empty matrix,
+ * ldx or ldq < cols, ld_scale < ceil(cols / 128), misaligned codes;
+ * SQZ_ERR_UNSUPPORTED for more than 65535 blocks of 128 rows;
+ * SQZ_ERR_CUDA.
+ */
+SQZ_API sqz_status sqz_fp8_quantize(const void* x, int32_t x_type, int64_t batch, int32_t rows, int32_t cols,
+                                    int64_t ldx, int32_t block_rows, int32_t format, uint8_t* q, int64_t ldq,
+                                    float* scale, int64_t ld_scale, void* stream);
+
+/* One operand of sqz_fp8_gemm (device pointers, owned by the caller). */
+typedef struct {
+    const uint8_t* q;     /* [rows][ld] codes                          */
+    int64_t ld;           /* >= k, a multiple of 16                    */
+    const float* scale;   /* [ceil(rows / block_rows)][ld_scale]       */
+    int64_t ld_scale;     /* >= ceil(k / 128)                          */
+    int32_t format;       /* SQZ_FP8_E4M3 or SQZ_FP8_E5M2              */
+} sqz_fp8_matrix;
+
+/*
+ * y = A W^T: A [m][k] with 1 x 128 blocks, W [n][k] with 128 x 128 blocks
+ * (the two formats may differ), y [m][ldy] of y_type (SQZ_TYPE_*), overwritten;
+ * y beyond column n is left as it is.  One launch, asynchronous on `stream`,
+ * no workspace: calls on different streams may overlap, and the call may be
+ * captured into a graph.  m from one row on; k need not be a multiple of 128.
+ * y must not overlap the operands.
+ *
+ * Arithmetic: products of codes are summed over a block of 128 by the tensor
+ * cores into fp32, the blocks' sums times the product of their two scales are
+ * added in fp32, and y is rounded once.  Bitwise reproducible.  NaN codes or
+ * scales make the outputs they enter NaN.
+ *
+ * Errors: SQZ_ERR_INVALID_ARG (NULL, negative or too small sizes and pitches,
+ * unknown formats or types, misaligned codes or y); SQZ_ERR_CUDA.  No
+ * synchronisation.
+ */
+SQZ_API sqz_status sqz_fp8_gemm(const sqz_fp8_matrix* a, const sqz_fp8_matrix* w, int32_t m, int32_t n, int32_t k,
+                                void* y, int64_t ldy, int32_t y_type, void* stream);
+
+/*
+ * Read and clear the current device's status word of sqz_fp8_gemm, ordered on
+ * `stream` (synchronises it; refused with SQZ_ERR_UNSUPPORTED on a stream
+ * under capture).  0 means every call so far completed normally; bit 0 (1)
+ * means that a bounded wait inside a kernel gave up and y of that call is
+ * undefined (the call then returns SQZ_ERR_TIMEOUT with *status set).
+ * Errors: SQZ_ERR_INVALID_ARG, SQZ_ERR_UNSUPPORTED, SQZ_ERR_CUDA,
+ * SQZ_ERR_TIMEOUT.
+ */
+SQZ_API sqz_status sqz_fp8_status(void* stream, int32_t* status);
+
 /* Message for the calling thread's last non-OK status ("" if none). */
 SQZ_API const char* sqz_last_error(void);
 

@@ -31,6 +31,11 @@ SQZ_MAC_CUDA_CORES = 1
 SQZ_MAC_MIXED = 2
 SQZ_CSR_BALANCED = 0
 SQZ_CSR_ROWWISE = 1
+SQZ_FP8_E4M3 = 0
+SQZ_FP8_E5M2 = 1
+SQZ_TYPE_F16 = 0
+SQZ_TYPE_BF16 = 1
+SQZ_TYPE_F32 = 2
 
 STATUS_NAMES = {0: "SQZ_OK", 1: "SQZ_ERR_INVALID_ARG", 2: "SQZ_ERR_UNSUPPORTED", 3: "SQZ_ERR_CUDA",
                 4: "SQZ_ERR_OOM", 5: "SQZ_ERR_TIMEOUT"}
@@ -39,7 +44,8 @@ STATUS_NAMES = {0: "SQZ_OK", 1: "SQZ_ERR_INVALID_ARG", 2: "SQZ_ERR_UNSUPPORTED",
 EXPORTED = ("sqz_create_layer", "sqz_gemv", "sqz_gemv_host", "sqz_debug_dequant", "sqz_layer_info",
             "sqz_destroy", "sqz_fp16_gemv", "sqz_last_error", "sqz_version", "sqz_check_csr_static",
             "sqz_layer_set_mac", "sqz_layer_set_csr_mode", "sqz_layer_status", "sqz_encode",
-            "sqz_encode_outliers", "sqz_plan_query", "sqz_layer_set_predecode", "sqz_tile_split_query")
+            "sqz_encode_outliers", "sqz_plan_query", "sqz_layer_set_predecode", "sqz_tile_split_query",
+            "sqz_fp8_quantize", "sqz_fp8_gemm", "sqz_fp8_status")
 
 
 class SqzError(RuntimeError):
@@ -65,6 +71,16 @@ class sqz_layer_desc(ctypes.Structure):
         ("rowptr", ctypes.c_void_p),
         ("col", ctypes.c_void_p),
         ("val", ctypes.c_void_p),
+    ]
+
+
+class sqz_fp8_matrix(ctypes.Structure):
+    _fields_ = [
+        ("q", ctypes.c_void_p),
+        ("ld", ctypes.c_int64),
+        ("scale", ctypes.c_void_p),
+        ("ld_scale", ctypes.c_int64),
+        ("format", ctypes.c_int32),
     ]
 
 
@@ -107,6 +123,13 @@ def lib() -> ctypes.CDLL:
         L.sqz_plan_query.restype = ctypes.c_int
         L.sqz_tile_split_query.argtypes = [P, i32, i32, i32, i32, P, ctypes.POINTER(i32)]
         L.sqz_tile_split_query.restype = ctypes.c_int
+        L.sqz_fp8_quantize.argtypes = [P, i32, i64, i32, i32, i64, i32, i32, P, i64, P, i64, P]
+        L.sqz_fp8_quantize.restype = ctypes.c_int
+        M = ctypes.POINTER(sqz_fp8_matrix)
+        L.sqz_fp8_gemm.argtypes = [M, M, i32, i32, i32, P, i64, i32, P]
+        L.sqz_fp8_gemm.restype = ctypes.c_int
+        L.sqz_fp8_status.argtypes = [P, ctypes.POINTER(i32)]
+        L.sqz_fp8_status.restype = ctypes.c_int
         L.sqz_encode_outliers.argtypes = [i64, ctypes.c_double]
         L.sqz_encode_outliers.restype = i64
         L.sqz_last_error.argtypes = []
@@ -382,4 +405,110 @@ def sqz_layer_set_predecode(layer: Layer, enable: int) -> None:
 def sqz_layer_status(layer: Layer, stream=None) -> int:
     st = ctypes.c_int32(-1)
     _check(lib().sqz_layer_status(layer, _stream(stream), ctypes.byref(st)), "sqz_layer_status")
+    return int(st.value)
+
+
+# ------------------------------------------------ 8-bit floating point, block scales
+_FP8_FORMATS = {torch.float8_e4m3fn: SQZ_FP8_E4M3, torch.float8_e5m2: SQZ_FP8_E5M2}
+_TYPES = {torch.float16: SQZ_TYPE_F16, torch.bfloat16: SQZ_TYPE_BF16, torch.float32: SQZ_TYPE_F32}
+
+
+def _on_current_device(t: torch.Tensor, name: str) -> None:
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+
+
+def _pitch(t: torch.Tensor, name: str) -> int:
+    """Elements from one row to the next of a tensor whose rows are contiguous and, beyond two
+    dimensions, evenly spaced."""
+    if t.dim() < 2:
+        raise ValueError(f"{name} must have at least two dimensions")
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name} must be row-major")
+    rows, ld = 1, None
+    for d in range(t.dim() - 2, -1, -1):
+        if t.shape[d] != 1:
+            if ld is None:
+                ld = t.stride(d) // rows if t.stride(d) % rows == 0 else -1
+            if t.stride(d) != rows * ld:
+                raise ValueError(f"{name} must have evenly spaced rows")
+        rows *= t.shape[d]
+    if ld is None:  # a single row
+        ld = (t.shape[-1] + 15) // 16 * 16
+    return ld
+
+
+def sqz_fp8_quantize(x: torch.Tensor, block_rows: int = 1, dtype: torch.dtype = torch.float8_e4m3fn,
+                     q: Optional[torch.Tensor] = None, scale: Optional[torch.Tensor] = None, stream=None):
+    """Quantize fp16/bf16 x [rows, cols] or [batch, rows, cols] (CUDA) to 8-bit codes with one fp32 scale per block of
+    block_rows (1 or 128) x 128; returns (q, scale).  q has x's shape and an fp8 dtype on a 16-byte row pitch;
+    scale is [(batch,) ceil(rows / block_rows), ceil(cols / 128)].  Both are allocated unless given (q's dtype
+    then names the format)."""
+    if x.dim() not in (2, 3):
+        raise ValueError("x must be [rows, cols] or [batch, rows, cols]")
+    _on_current_device(x, "x")
+    if x.dtype not in _TYPES or x.dtype == torch.float32:
+        raise TypeError(f"x has dtype {x.dtype}, expected fp16 or bf16")
+    if block_rows not in (1, 128):
+        raise ValueError("block_rows must be 1 or 128")
+    rows, cols = x.shape[-2:]
+    if q is None:
+        if dtype not in _FP8_FORMATS:
+            raise TypeError(f"dtype {dtype} is not an 8-bit floating-point type")
+        q = torch.empty((*x.shape[:-1], (cols + 15) // 16 * 16), dtype=dtype, device=x.device)[..., :cols]
+    else:
+        _on_current_device(q, "q")
+        if q.dtype not in _FP8_FORMATS or q.shape != x.shape:
+            raise ValueError(f"q must have shape {tuple(x.shape)} and an fp8 dtype")
+    shape = (*x.shape[:-2], -(-rows // block_rows), -(-cols // 128))
+    if scale is None:
+        scale = torch.empty(shape, dtype=torch.float32, device=x.device)
+    else:
+        _on_current_device(scale, "scale")
+        if scale.dtype != torch.float32 or tuple(scale.shape) != shape:
+            raise ValueError(f"scale must be fp32 of shape {shape}")
+    if x.numel():
+        _check(lib().sqz_fp8_quantize(x.data_ptr(), _TYPES[x.dtype], x.shape[0] if x.dim() == 3 else 1, rows, cols,
+                                      _pitch(x, "x"), block_rows, _FP8_FORMATS[q.dtype], q.data_ptr(), _pitch(q, "q"),
+                                      scale.data_ptr(), _scale_pitch(scale), _stream(stream)), "sqz_fp8_quantize")
+    return q, scale
+
+
+def _scale_pitch(t: torch.Tensor) -> int:
+    return max(_pitch(t, "scale"), t.shape[-1])
+
+
+def _fp8_matrix(q: torch.Tensor, scale: torch.Tensor, name: str, block_rows: int) -> sqz_fp8_matrix:
+    _on_current_device(q, name)
+    _on_current_device(scale, f"{name}_scale")
+    if q.dtype not in _FP8_FORMATS:
+        raise TypeError(f"{name} has dtype {q.dtype}, expected float8_e4m3fn or float8_e5m2")
+    if q.dim() != 2 or scale.dtype != torch.float32 or \
+            scale.shape != (-(-q.shape[0] // block_rows), -(-q.shape[1] // 128)):
+        raise ValueError(f"{name} must be [rows, k] with fp32 scales [ceil(rows / {block_rows}), ceil(k / 128)], got "
+                         f"{tuple(q.shape)} and {tuple(scale.shape)}")
+    return sqz_fp8_matrix(q.data_ptr(), _pitch(q, name), scale.data_ptr(), _scale_pitch(scale), _FP8_FORMATS[q.dtype])
+
+
+def sqz_fp8_gemm(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor, y: torch.Tensor,
+                 stream=None) -> None:
+    """y [m, n] (fp16, bf16 or fp32) = A W^T of 8-bit matrices a [m, k] (scales [m, ceil(k/128)]) and w [n, k]
+    (scales [ceil(n/128), ceil(k/128)])."""
+    A, W = _fp8_matrix(a, a_scale, "a", 1), _fp8_matrix(w, w_scale, "w", 128)
+    (m, k), n = a.shape, w.shape[0]
+    _on_current_device(y, "y")
+    if w.shape[1] != k or y.shape != (m, n):
+        raise ValueError(f"a {tuple(a.shape)}, w {tuple(w.shape)} and y {tuple(y.shape)} do not fit together")
+    if y.dtype not in _TYPES:
+        raise TypeError(f"y has dtype {y.dtype}, expected fp16, bf16 or fp32")
+    ldy = max(_pitch(y, "y"), n)
+    _check(lib().sqz_fp8_gemm(ctypes.byref(A), ctypes.byref(W), m, n, k, y.data_ptr(), ldy, _TYPES[y.dtype],
+                              _stream(stream)), "sqz_fp8_gemm")
+
+
+def sqz_fp8_status(stream=None) -> int:
+    st = ctypes.c_int32(-1)
+    _check(lib().sqz_fp8_status(_stream(stream), ctypes.byref(st)), "sqz_fp8_status")
     return int(st.value)

@@ -1,0 +1,198 @@
+// fp8_common.cuh -- device helpers shared by the block-scaled 8-bit kernels:
+// tensor maps' tile loads, tcgen05 matrix instructions on 8-bit operands and
+// their accumulators in tensor memory, bounded waits, cluster barriers.
+//
+// Operand tiles.  A tile is 128 bytes (128 codes, one scale block) of K by R
+// rows, brought in by TMA with the 128-byte swizzle: row r at byte 128 r, its
+// 16-byte chunk c at chunk c ^ (r % 8).  The matrix descriptor below says so:
+// K-major, groups of 8 rows 1024 bytes apart, tiles 1024-byte aligned.  One
+// tcgen05.mma takes 32 codes of K; the next 32 start 32 bytes further into
+// the swizzle atom.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <stdint.h>
+
+#include "common.cuh"
+#include "ptx.cuh"
+
+namespace sqz {
+namespace f8 {
+
+using tc::fence_mbar_init;
+using tc::mbar_arrive;
+using tc::mbar_expect_tx;
+using tc::mbar_init;
+using tc::mbar_try_wait;
+using tc::pdl_launch_dependents;
+using tc::pdl_wait_previous;
+using tc::smem_u32;
+
+constexpr int kBlockK = 128;          // codes of K per scale block = bytes of a tile row
+constexpr int kTileBytes = 128 * 128; // a tile of 128 rows
+
+enum OutType : int { kF16 = 0, kBF16 = 1, kF32 = 2 };
+
+// Waits are bounded (tc::kWaitLimit polls of tc::kSuspendNs, about two
+// seconds).  A wait that gives up sets `*dead` (shared memory), which ends
+// the other waits of the CTA too; the kernel then leaves in order.
+__device__ __forceinline__ bool wait_alive(uint64_t* bar, uint32_t parity, volatile int* dead) {
+    for (uint32_t i = 0; i < tc::kWaitLimit; ++i) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if (*dead) return false;
+    }
+    *dead = 1;
+    return false;
+}
+
+// After a wait gave up: time (100 ms) for the thread's own copies and matrix
+// instructions in flight to end before the CTA frees its memory and leaves.
+__device__ __forceinline__ void let_copies_land() {
+    for (int i = 0; i < 100; ++i) __nanosleep(1000000);
+}
+
+// ------------------------------------------------------------------- TMA
+__device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(
+            smem_u32(dst)),
+        "l"(map), "r"(smem_u32(bar)), "r"(x), "r"(y)
+        : "memory");
+}
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y, int z) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], "
+        "[%2];" ::"r"(smem_u32(dst)),
+        "l"(map), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
+        : "memory");
+}
+__device__ __forceinline__ void tma_prefetch_map(const CUtensorMap* map) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
+// Asynchronous 4-byte copy to shared memory; `valid` false writes zero.  The
+// thread's arrival on `bar` is posted when its copies so far have landed (it
+// counts as one of the barrier's expected arrivals).
+__device__ __forceinline__ void cp_async4(void* dst, const void* src, bool valid) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(valid ? 4 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+// --------------------------------------------------------------- tcgen05
+__device__ __forceinline__ void tmem_alloc(uint32_t* dst, uint32_t cols) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst)), "r"(cols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc(uint32_t taddr, uint32_t cols) {
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(cols) : "memory");
+}
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+// Descriptor of a swizzled K-major operand tile at a shared-memory address
+// (bits 0-13 address / 16, 32-45 byte distance of 8-row groups / 16 = 64,
+// 46-47 version 1, 61-63 layout 2 = 128-byte swizzle).
+__device__ __forceinline__ uint64_t operand_desc(uint32_t addr) {
+    return (uint64_t)((addr >> 4) & 0x3FFF) | (1ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
+}
+// Instruction descriptor of kind::f8f6f4, fp32 accumulators, both operands
+// K-major: bits 4-5 accumulator type 1, 7-9 / 10-12 operand formats (0 e4m3,
+// 1 e5m2), 17-22 N / 8, 24-28 M / 16.
+__host__ __device__ inline uint32_t instr_desc(int a_format, int b_format, int m, int n) {
+    return (1u << 4) | ((uint32_t)a_format << 7) | ((uint32_t)b_format << 10) | ((uint32_t)(n >> 3) << 17) |
+           ((uint32_t)(m >> 4) << 24);
+}
+__device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate ? 1 : 0)
+        : "memory");
+}
+// A whole 128-code block of K: four instructions, the first one overwriting.
+__device__ __forceinline__ void mma_block(uint32_t d, uint32_t a_addr, uint32_t b_addr, uint32_t idesc) {
+    const uint64_t a = operand_desc(a_addr), b = operand_desc(b_addr);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) mma_f8(d, a + 2 * k, b + 2 * k, idesc, k > 0);
+}
+// One arrival on `bar` when the thread's matrix instructions so far are done.
+__device__ __forceinline__ void mma_commit(uint64_t* bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
+                 : "memory");
+}
+
+// 16 or 32 consecutive columns of the warp's 32 lanes (lane = row).
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+}
+// Wait for this thread's tcgen05.ld; the registers pass through so that no
+// use of them is scheduled before it.
+__device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[16]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+                 :
+                 : "memory");
+}
+
+// ------------------------------------------------------------ arithmetic
+// (a0, a1) += (d0, d1) * (s, s): one instruction for two fp32 fused
+// multiply-adds, each rounded as fmaf.
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t pack2u(uint32_t a, uint32_t b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& a, float& b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ void fma2(uint64_t& acc, uint64_t d, uint64_t s) {
+    asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc) : "l"(d), "l"(s));
+}
+
+// -------------------------------------------------------------- clusters
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The value at the same shared-memory address in CTA `rank` of the cluster.
+__device__ __forceinline__ float ld_cluster(uint32_t addr, uint32_t rank) {
+    uint32_t remote;
+    float v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(addr), "r"(rank));
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(remote) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ void store_out(void* y, int64_t at, int type, float v) {
+    if (type == kF16)
+        static_cast<__half*>(y)[at] = __float2half_rn(v);
+    else if (type == kBF16)
+        static_cast<__nv_bfloat16*>(y)[at] = __float2bfloat16_rn(v);
+    else
+        static_cast<float*>(y)[at] = v;
+}
+
+}  // namespace f8
+}  // namespace sqz

@@ -1,0 +1,564 @@
+// kernels_fp8.cuh -- 8-bit floating point with one fp32 scale per block of
+// 128 columns: the quantizer and the matrix product.
+#pragma once
+
+#include "fp8_common.cuh"
+
+namespace sqz {
+namespace f8 {
+
+// ------------------------------------------------------------- quantizer
+// scale = max|x| / F over a block (F the largest finite code; 1 for a block
+// of zeros), code = x / scale rounded to nearest even.
+//
+// The maximum is taken over the values' bit patterns without the sign: the
+// order of non-negative floats is that of their bits, and NaN, above
+// infinity, wins, so a block that holds one gets a NaN scale.
+//
+// The quotient: with y = 1 / scale correctly rounded and q0 = x y,
+// q0 - (q0 scale - x) y is x / scale correctly rounded (Markstein 1990) as
+// long as no step under- or overflows: three operations where a division
+// takes over ten (the kernel would be bound by them, not by its 3 bytes per
+// element).  Blocks whose scale is outside [2^-100, 2^120] (or NaN, or
+// infinite) divide.  Quotients below 2^-24 of the largest need no exactness:
+// they round to code 0 either way.
+struct Quotient {
+    float scale, inv;
+    bool plain;
+    __device__ __forceinline__ explicit Quotient(float s) : scale(s), inv(1.f / s) {
+        plain = !(s >= 0x1p-100f && s <= 0x1p120f);
+    }
+    __device__ __forceinline__ float operator()(float x) const {
+        if (plain) return x / scale;
+        const float q = x * inv;
+        return fmaf(-fmaf(q, scale, -x), inv, q);  // the remainder's sign keeps -0 / scale = -0
+    }
+};
+
+template <bool E5M2>
+__device__ __forceinline__ uint32_t code2(float lo, float hi) {
+    uint16_t r;
+    if (E5M2)
+        asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    else
+        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+template <bool BF16>
+__device__ __forceinline__ float x_to_float(uint32_t h) {
+    if (BF16) return __uint_as_float(h << 16);
+    return __half2float(__ushort_as_half((uint16_t)h));
+}
+
+// Eight consecutive elements of row `r` from column c (zeros past the edge).
+template <bool BF16, bool VEC>
+__device__ __forceinline__ void load8(const uint16_t* __restrict__ row, int c, int cols, float (&v)[8]) {
+    if (VEC && c + 8 <= cols) {
+        const uint4 u = ldg_stream_u128(row + c);
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[2 * i] = x_to_float<BF16>(w[i] & 0xFFFF);
+            v[2 * i + 1] = x_to_float<BF16>(w[i] >> 16);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = c + i < cols ? x_to_float<BF16>(__ldg(row + c + i)) : 0.f;
+    }
+}
+
+template <bool E5M2>
+__device__ __forceinline__ void store8(uint8_t* __restrict__ row, int c, int cols, const float (&v)[8],
+                                       const Quotient& by) {
+    uint32_t lo = 0, hi = 0;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        lo |= code2<E5M2>(by(v[2 * i]), by(v[2 * i + 1])) << (16 * i);
+        hi |= code2<E5M2>(by(v[4 + 2 * i]), by(v[4 + 2 * i + 1])) << (16 * i);
+    }
+    if (c + 8 <= cols) {
+        *reinterpret_cast<uint2*>(row + c) = make_uint2(lo, hi);  // rows are 16-byte aligned
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (c + i < cols) row[c + i] = (uint8_t)((i < 4 ? lo >> (8 * i) : hi >> (8 * (i - 4))) & 0xFF);
+    }
+}
+
+__device__ __forceinline__ uint32_t max_bits8(const float (&v)[8], uint32_t m) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+    return m;
+}
+
+template <bool E5M2>
+__device__ __forceinline__ float scale_of(uint32_t max_bits) {
+    return max_bits ? __uint_as_float(max_bits) / (E5M2 ? 57344.f : 448.f) : 1.f;
+}
+
+struct QuantParams {
+    const uint16_t* x;
+    int64_t ldx;
+    uint8_t* q;
+    int64_t ldq;
+    float* scale;
+    int64_t lds;
+    int64_t batch;
+    int rows, cols, nblocks;  // nblocks = scale blocks of a row
+};
+
+// Blocks of 1 x 128: 16 lanes hold a block, 8 elements each; a warp takes two
+// blocks a step and strides over all rows x blocks.
+template <bool BF16, bool E5M2, bool VEC>
+__global__ void __launch_bounds__(256) fp8_quantize_rows_kernel(const QuantParams p) {
+    pdl_launch_dependents();
+    pdl_wait_previous();
+    const int lane16 = threadIdx.x & 15;
+    const int64_t total = p.batch * p.rows * p.nblocks;
+    const bool narrow = total <= 0x7fffffff;  // 32-bit division (the 64-bit one costs as much as a block)
+    const int64_t step = (int64_t)gridDim.x * (blockDim.x / 16);
+    // the loop's bound is the same for the whole warp: its shuffles need every lane
+    for (int64_t first = (int64_t)blockIdx.x * (blockDim.x / 16) + (threadIdx.x / 32) * 2; first < total;
+         first += step) {
+        const int64_t at = first + ((threadIdx.x >> 4) & 1);
+        const bool live = at < total;
+        const int64_t row = !live ? 0 : narrow ? (int64_t)((uint32_t)at / (uint32_t)p.nblocks) : at / p.nblocks;
+        const int b = live ? (int)(at - row * p.nblocks) : 0;
+        const int c = b * kBlockK + lane16 * 8;
+        float v[8];
+        load8<BF16, VEC>(p.x + row * p.ldx, c, p.cols, v);
+        uint32_t m = max_bits8(v, 0);
+#pragma unroll
+        for (int off = 8; off > 0; off >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, off));
+        const float s = scale_of<E5M2>(m);
+        if (!live) continue;
+        if (c < p.cols) store8<E5M2>(p.q + row * p.ldq, c, p.cols, v, Quotient(s));
+        if (lane16 == 0) p.scale[row * p.lds + b] = s;
+    }
+}
+
+// Blocks of 128 x 128: one CTA per block, the block in registers (64 elements
+// a thread) between the maximum and the division, so x is read once.
+template <bool BF16, bool E5M2, bool VEC>
+__global__ void __launch_bounds__(256) fp8_quantize_tiles_kernel(const QuantParams p) {
+    pdl_launch_dependents();
+    pdl_wait_previous();
+    __shared__ uint32_t part[8];
+    const int row_blocks = (p.rows + 127) / 128;
+    const int64_t z = blockIdx.y / row_blocks;
+    const int rb = (int)(blockIdx.y - z * row_blocks), b = blockIdx.x;
+    const int r0 = rb * 128 + (threadIdx.x >> 4), c = b * kBlockK + (threadIdx.x & 15) * 8;
+    const uint16_t* x = p.x + z * p.rows * p.ldx;
+    uint8_t* q = p.q + z * p.rows * p.ldq;
+    float v[8][8];
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int r = r0 + 16 * i;
+        if (r < p.rows) {
+            load8<BF16, VEC>(x + (int64_t)r * p.ldx, c, p.cols, v[i]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[i][j] = 0.f;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = max_bits8(v[i], m);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, off));
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = m;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = max(m, part[i]);
+    const float s = scale_of<E5M2>(m);
+    const Quotient by(s);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int r = r0 + 16 * i;
+        if (r < p.rows && c < p.cols) store8<E5M2>(q + (int64_t)r * p.ldq, c, p.cols, v[i], by);
+    }
+    if (threadIdx.x == 0) p.scale[(z * row_blocks + rb) * p.lds + b] = s;
+}
+
+// -------------------------------------------------------- matrix product
+// y[m][n] = sum_b sa[m][b] sw[n / 128][b] * (sum over the 128 k of block b of
+// a[m][k] w[n][k]).  The inner sum is four tcgen05 matrix instructions into
+// tensor memory; the outer one is carried in fp32 registers, one fused
+// multiply-add per output and block ("promotion").
+
+struct GemmParams {
+    const float* sa;
+    int64_t ld_sa;
+    const float* sw;
+    int64_t ld_sw;
+    void* y;
+    int64_t ldy;
+    int* status;
+    int m, n, nkb;  // nkb = blocks of K
+    int out_type;
+    uint32_t idesc;
+    int stages;
+    int tiles_m, tiles_n;  // many-row kernel
+    int vec_out;           // y rows are 16-byte aligned
+};
+
+constexpr int kMaxStages = 12;
+
+// Few rows of A (up to 128 per token tile): bound by reading W.  The weights
+// take the 128 lanes (MMA "A", 128 rows of W) and the TB tokens the columns,
+// so a tile costs the tensor cores little however few tokens there are, and
+// the K axis is split over the CTAs of a cluster, whose partial sums meet in
+// distributed shared memory in rank order: no workspace, no atomics, the same
+// bits every run.
+//
+//   warp 0: TMA loads of W and A tiles into a ring of stages
+//   warp 1: TMEM allocation, matrix instructions into one of two accumulators
+//   warp 2: the block's scales into the stage (4-byte asynchronous copies)
+//   warps 3-6: promotion; thread = a row of W
+template <int TB>
+struct FewShape {
+    static constexpr int kStageBytes = kTileBytes + TB * kBlockK;
+    static constexpr int kScaleFloats = TB + 4;  // TB token scales, the weights' scale
+    static constexpr int kTmemCols = 2 * TB < 32 ? 32 : 2 * TB;
+    static constexpr int kThreads = 224;
+    static int smem_bytes(int stages) { return 1024 + stages * (kStageBytes + kScaleFloats * 4); }
+};
+
+template <int TB>
+__global__ void __launch_bounds__(224) fp8_gemm_few_kernel(const __grid_constant__ CUtensorMap map_w,
+                                                            const __grid_constant__ CUtensorMap map_a,
+                                                            const GemmParams p) {
+    using S = FewShape<TB>;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ uint64_t full[kMaxStages], empty[kMaxStages], tfull[2], tempty[2];
+    __shared__ uint32_t taddr_s;
+    __shared__ int dead_s;
+    uint8_t* ring = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+    float* scales = reinterpret_cast<float*>(ring + p.stages * S::kStageBytes);
+    volatile int* dead = &dead_s;
+
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int splits = gridDim.x, rank = blockIdx.x;
+    const int row0 = blockIdx.y * 128, tok0 = blockIdx.z * TB;
+    const int kb0 = (int)((int64_t)p.nkb * rank / splits), kb1 = (int)((int64_t)p.nkb * (rank + 1) / splits);
+    const int nk = kb1 - kb0;
+
+    if (warp == 1) tmem_alloc(&taddr_s, S::kTmemCols);
+    if (threadIdx.x == 0) {
+        dead_s = 0;
+        for (int i = 0; i < p.stages; ++i) {
+            mbar_init(&full[i], 1 + 32);
+            mbar_init(&empty[i], 1 + 4);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&tfull[i], 1);
+            mbar_init(&tempty[i], 4);
+        }
+        fence_mbar_init();
+        tma_prefetch_map(&map_w);
+        tma_prefetch_map(&map_a);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t taddr = taddr_s;
+    pdl_launch_dependents();
+    pdl_wait_previous();
+
+    float acc[TB];
+    if (warp == 0) {
+        if (lane == 0) {
+            int st = 0, ph = 0, it = 0;
+            for (; it < nk; ++it) {
+                if (!wait_alive(&empty[st], ph ^ 1, dead)) break;
+                mbar_expect_tx(&full[st], S::kStageBytes);
+                uint8_t* at = ring + st * S::kStageBytes;
+                tma_load_2d(at, &map_w, &full[st], (kb0 + it) * kBlockK, row0);
+                tma_load_2d(at + kTileBytes, &map_a, &full[st], (kb0 + it) * kBlockK, tok0);
+                if (++st == p.stages) st = 0, ph ^= 1;
+            }
+            if (it < nk) let_copies_land();
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            int st = 0, ph = 0;
+            for (int it = 0; it < nk; ++it) {
+                const int buf = it & 1;
+                if (!wait_alive(&tempty[buf], ((it >> 1) & 1) ^ 1, dead) || !wait_alive(&full[st], ph, dead)) {
+                    let_copies_land();
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t at = smem_u32(ring + st * S::kStageBytes);
+                mma_block(taddr + buf * TB, at, at + kTileBytes, p.idesc);
+                mma_commit(&empty[st]);
+                mma_commit(&tfull[buf]);
+                if (++st == p.stages) st = 0, ph ^= 1;
+            }
+        }
+    } else if (warp == 2) {
+        int st = 0, ph = 0;
+        const float* sw = p.sw + (int64_t)blockIdx.y * p.ld_sw;
+        for (int it = 0; it < nk; ++it) {
+            if (!__all_sync(0xffffffffu, wait_alive(&empty[st], ph ^ 1, dead))) break;
+            float* dst = scales + st * S::kScaleFloats;
+            const int kb = kb0 + it;
+#pragma unroll
+            for (int t = lane; t < TB; t += 32) {
+                const bool ok = tok0 + t < p.m;
+                cp_async4(dst + t, p.sa + (ok ? (int64_t)(tok0 + t) * p.ld_sa + kb : 0), ok);
+            }
+            if (lane == 0) cp_async4(dst + TB, sw + kb, true);
+            cp_async_arrive(&full[st]);
+            if (++st == p.stages) st = 0, ph ^= 1;
+        }
+    } else {
+#pragma unroll
+        for (int t = 0; t < TB; ++t) acc[t] = 0.f;
+        const uint32_t lanes = taddr + ((uint32_t)(warp & 3) << 21);
+        int st = 0, ph = 0;
+        for (int it = 0; it < nk; ++it) {
+            const int buf = it & 1;
+            bool ok = wait_alive(&full[st], ph, dead);  // the scales of the stage
+            ok = ok && wait_alive(&tfull[buf], (it >> 1) & 1, dead);
+            if (!__all_sync(0xffffffffu, ok)) break;
+            tc_fence_after();
+            const float* sc = scales + st * S::kScaleFloats;
+            const float sw = sc[TB];
+#pragma unroll
+            for (int c = 0; c < TB; c += 16) {
+                uint32_t d[16];
+                tmem_ld16(lanes + buf * TB + c, d);
+                tmem_wait_ld(d);
+#pragma unroll
+                for (int j = 0; j < 16; ++j) acc[c + j] = fmaf(__uint_as_float(d[j]), sc[c + j] * sw, acc[c + j]);
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&tempty[buf]);
+                mbar_arrive(&empty[st]);
+            }
+            if (++st == p.stages) st = 0, ph ^= 1;
+        }
+    }
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc(taddr, S::kTmemCols);
+    if (threadIdx.x == 0 && *dead) atomicOr(p.status, 1);
+
+    const int tokens = min(TB, p.m - tok0);
+    const int r = (warp & 3) * 32 + lane;  // row of W in the tile (promotion warps)
+    if (splits == 1) {
+        if (warp >= 3 && row0 + r < p.n) {
+#pragma unroll
+            for (int t = 0; t < TB; ++t)
+                if (t < tokens) store_out(p.y, (int64_t)(tok0 + t) * p.ldy + row0 + r, p.out_type, acc[t]);
+        }
+        return;
+    }
+    float* red = reinterpret_cast<float*>(ring);  // every copy into the ring has been read
+    if (warp >= 3) {
+#pragma unroll
+        for (int t = 0; t < TB; ++t)
+            if (t < tokens) red[t * 128 + r] = acc[t];
+    }
+    cluster_sync();
+    const int rows = 128 / splits;  // splits is a power of two
+    for (int i = threadIdx.x; i < rows * tokens; i += S::kThreads) {
+        const int t = i / rows, rr = rank * rows + i % rows;
+        if (row0 + rr >= p.n) continue;
+        float v = 0.f;
+        for (int c = 0; c < splits; ++c) v += ld_cluster(smem_u32(red + t * 128 + rr), c);
+        store_out(p.y, (int64_t)(tok0 + t) * p.ldy + row0 + rr, p.out_type, v);
+    }
+    cluster_sync();  // the other CTAs have read this one's sums
+}
+
+// Many rows of A: bound by the tensor cores and by the promotion.  Tiles of
+// 128 rows of A x BN rows of W, a persistent CTA per SM.  A thread of the
+// promotion holds one row of A and BN / 2 columns: the block's scale is then
+// one number per thread (the row's scale times the scale of the 128 rows of W
+// that its columns lie in), and the multiply-adds go two to an instruction.
+// Two accumulators in tensor memory let the matrix instructions of block b+1
+// run under the promotion of block b.
+//
+//   warp 0: TMA ring, warp 1: TMEM and matrix instructions, warps 2-9:
+//   promotion (warp % 4 = the 32 lanes it may read; first or second half of
+//   the columns)
+template <int BN>
+struct ManyShape {
+    static constexpr int kStageBytes = kTileBytes + BN * kBlockK;
+    static constexpr int kTmemCols = 2 * BN;
+    static constexpr int kThreads = 320;
+    static constexpr int kCols = BN / 2;  // columns of a thread
+    static int smem_bytes(int stages) { return 1024 + stages * kStageBytes; }
+};
+
+template <int BN>
+__global__ void __launch_bounds__(320, 1) fp8_gemm_many_kernel(const __grid_constant__ CUtensorMap map_w,
+                                                                const __grid_constant__ CUtensorMap map_a,
+                                                                const GemmParams p) {
+    using S = ManyShape<BN>;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ uint64_t full[kMaxStages], empty[kMaxStages], tfull[2], tempty[2];
+    __shared__ uint32_t taddr_s;
+    __shared__ int dead_s;
+    uint8_t* ring = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+    volatile int* dead = &dead_s;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n;
+
+    if (warp == 1) tmem_alloc(&taddr_s, S::kTmemCols);
+    if (threadIdx.x == 0) {
+        dead_s = 0;
+        for (int i = 0; i < p.stages; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&tfull[i], 1);
+            mbar_init(&tempty[i], 8);
+        }
+        fence_mbar_init();
+        tma_prefetch_map(&map_w);
+        tma_prefetch_map(&map_a);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t taddr = taddr_s;
+    pdl_launch_dependents();
+    pdl_wait_previous();
+
+    if (warp == 0) {
+        if (lane == 0) {
+            int st = 0, ph = 0;
+            bool alive = true;
+            for (int64_t tile = blockIdx.x; tile < tiles && alive; tile += gridDim.x) {
+                const int tn = (int)(tile / p.tiles_m), tm = (int)(tile - (int64_t)tn * p.tiles_m);
+                for (int kb = 0; kb < p.nkb; ++kb) {
+                    if (!(alive = wait_alive(&empty[st], ph ^ 1, dead))) break;
+                    mbar_expect_tx(&full[st], S::kStageBytes);
+                    uint8_t* at = ring + st * S::kStageBytes;
+                    tma_load_2d(at, &map_a, &full[st], kb * kBlockK, tm * 128);
+                    tma_load_2d(at + kTileBytes, &map_w, &full[st], kb * kBlockK, tn * BN);
+                    if (++st == p.stages) st = 0, ph ^= 1;
+                }
+            }
+            if (!alive) let_copies_land();
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            int st = 0, ph = 0;
+            uint32_t it = 0;
+            bool alive = true;
+            for (int64_t tile = blockIdx.x; tile < tiles && alive; tile += gridDim.x) {
+                for (int kb = 0; kb < p.nkb; ++kb, ++it) {
+                    const int buf = it & 1;
+                    alive = wait_alive(&tempty[buf], ((it >> 1) & 1) ^ 1, dead) && wait_alive(&full[st], ph, dead);
+                    if (!alive) {
+                        let_copies_land();
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t at = smem_u32(ring + st * S::kStageBytes);
+                    mma_block(taddr + buf * BN, at, at + kTileBytes, p.idesc);
+                    mma_commit(&empty[st]);
+                    mma_commit(&tfull[buf]);
+                    if (++st == p.stages) st = 0, ph ^= 1;
+                }
+            }
+        }
+    } else {
+        const int half = (warp - 2) / 4;
+        const int r = (warp & 3) * 32 + lane;
+        const uint32_t lanes = taddr + ((uint32_t)(warp & 3) << 21) + half * S::kCols;
+        uint32_t it = 0;
+        bool alive = true;
+        for (int64_t tile = blockIdx.x; tile < tiles && alive; tile += gridDim.x) {
+            const int tn = (int)(tile / p.tiles_m), tm = (int)(tile - (int64_t)tn * p.tiles_m);
+            const int64_t row = (int64_t)tm * 128 + r;
+            const int col0 = tn * BN + half * S::kCols;
+            const bool row_ok = row < p.m;
+            const float* sa = p.sa + (row_ok ? row : 0) * p.ld_sa;
+            // the columns of a thread lie in one 128-row block of W
+            const float* sw = p.sw + (int64_t)min(col0 / 128, (p.n - 1) / 128) * p.ld_sw;
+            uint64_t acc[S::kCols / 2];
+#pragma unroll
+            for (int j = 0; j < S::kCols / 2; ++j) acc[j] = 0;
+            float s_next = __ldg(sa) * __ldg(sw);
+            for (int kb = 0; kb < p.nkb; ++kb, ++it) {
+                const int buf = it & 1;
+                const float s = s_next;
+                if (kb + 1 < p.nkb) s_next = __ldg(sa + kb + 1) * __ldg(sw + kb + 1);
+                if (!(alive = __all_sync(0xffffffffu, wait_alive(&tfull[buf], (it >> 1) & 1, dead)))) break;
+                tc_fence_after();
+                const uint64_t ss = pack2(s, s);
+                uint32_t d[2][16];
+                tmem_ld16(lanes + buf * BN, d[0]);
+#pragma unroll
+                for (int c = 0; c < S::kCols / 16; ++c) {
+                    tmem_wait_ld(d[c & 1]);
+                    if (c + 1 < S::kCols / 16) tmem_ld16(lanes + buf * BN + (c + 1) * 16, d[(c + 1) & 1]);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        fma2(acc[c * 8 + j], pack2u(d[c & 1][2 * j], d[c & 1][2 * j + 1]), ss);
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&tempty[buf]);
+            }
+            if (!alive || !row_ok) continue;
+            const int64_t at = row * p.ldy + col0;
+            const int left = p.n - col0;
+            if (p.vec_out && left >= S::kCols) {
+                if (p.out_type == kF32) {
+                    float4* y = reinterpret_cast<float4*>(static_cast<float*>(p.y) + at);
+#pragma unroll
+                    for (int j = 0; j < S::kCols / 4; ++j) {
+                        float4 v;
+                        unpack2(acc[2 * j], v.x, v.y);
+                        unpack2(acc[2 * j + 1], v.z, v.w);
+                        y[j] = v;
+                    }
+                } else {
+                    uint4* y = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.y) + at);
+#pragma unroll
+                    for (int j = 0; j < S::kCols / 8; ++j) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            float lo, hi;
+                            unpack2(acc[4 * j + i], lo, hi);
+                            if (p.out_type == kF16) {
+                                const __half2 h = __floats2half2_rn(lo, hi);
+                                w[i] = *reinterpret_cast<const uint32_t*>(&h);
+                            } else {
+                                const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+                                w[i] = *reinterpret_cast<const uint32_t*>(&h);
+                            }
+                        }
+                        y[j] = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < S::kCols / 2; ++j) {
+                    float lo, hi;
+                    unpack2(acc[j], lo, hi);
+                    if (2 * j < left) store_out(p.y, at + 2 * j, p.out_type, lo);
+                    if (2 * j + 1 < left) store_out(p.y, at + 2 * j + 1, p.out_type, hi);
+                }
+            }
+        }
+    }
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc(taddr, S::kTmemCols);
+    if (threadIdx.x == 0 && *dead) atomicOr(p.status, 1);
+}
+
+}  // namespace f8
+}  // namespace sqz

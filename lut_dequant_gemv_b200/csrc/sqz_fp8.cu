@@ -1,0 +1,285 @@
+// sqz_fp8.cu -- host side of the block-scaled 8-bit quantizer and matrix
+// product declared in include/sqz.h.  Every argument is checked on the host
+// before any CUDA call.
+#include "fp8_host.cuh"
+#include "kernels_fp8.cuh"
+
+namespace {
+
+using namespace sqz::f8;
+
+// Set by a kernel whose bounded wait gave up; read and cleared by
+// sqz_fp8_status.  One word per GPU.
+__device__ int g_fp8_status;
+
+sqz_status status_word(int** out) {
+    void* p = nullptr;
+    SQZ_F8_TRY(cudaGetSymbolAddress(&p, g_fp8_status), "cudaGetSymbolAddress(fp8 status)");
+    *out = static_cast<int*>(p);
+    return SQZ_OK;
+}
+
+bool aligned16(const void* p, int64_t ld) { return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % 16 == 0; }
+
+template <class Params>
+cudaError_t launch(void (*kernel)(const Params), dim3 grid, int threads, const Params& prm, cudaStream_t s) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, prm);
+}
+
+template <bool BF16, bool E5M2, bool VEC>
+cudaError_t launch_quantize(const QuantParams& p, int block_rows, int sms, cudaStream_t s) {
+    if (block_rows == 1) {
+        const int64_t warps = (p.batch * p.rows * p.nblocks + 1) / 2, ctas = (warps + 7) / 8;
+        const int64_t most = (int64_t)sms * 8 * 4;  // four rounds of the resident CTAs, then each strides
+        return launch(fp8_quantize_rows_kernel<BF16, E5M2, VEC>, dim3((unsigned)(ctas < most ? ctas : most)), 256, p, s);
+    }
+    return launch(fp8_quantize_tiles_kernel<BF16, E5M2, VEC>,
+                  dim3((unsigned)p.nblocks, (unsigned)(p.batch * ((p.rows + 127) / 128))), 256, p, s);
+}
+
+// ------------------------------------------------------------ the product
+int round_pow2(int v) {
+    int p = 16;
+    while (p < v) p *= 2;
+    return p;
+}
+
+template <int TB>
+sqz_status launch_few(const CUtensorMap& mw, const CUtensorMap& ma, GemmParams p, int splits, int stages,
+                      const DeviceSizes& d, cudaStream_t s) {
+    static std::atomic<uint64_t> ready;
+    const sqz_status st = allow_smem(fp8_gemm_few_kernel<TB>, d, &ready);
+    if (st != SQZ_OK) return st;
+    p.stages = stages;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)splits, (unsigned)((p.n + 127) / 128), (unsigned)((p.m + TB - 1) / TB));
+    cfg.blockDim = dim3(FewShape<TB>::kThreads);
+    cfg.dynamicSmemBytes = (size_t)FewShape<TB>::smem_bytes(stages);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)splits;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    SQZ_F8_TRY(cudaLaunchKernelEx(&cfg, fp8_gemm_few_kernel<TB>, mw, ma, p), "fp8 product launch");
+    return SQZ_OK;
+}
+
+template <int BN>
+sqz_status launch_many(const CUtensorMap& mw, const CUtensorMap& ma, GemmParams p, const DeviceSizes& d,
+                       cudaStream_t s) {
+    static std::atomic<uint64_t> ready;
+    const sqz_status st = allow_smem(fp8_gemm_many_kernel<BN>, d, &ready);
+    if (st != SQZ_OK) return st;
+    p.tiles_m = (p.m + 127) / 128;
+    p.tiles_n = (p.n + BN - 1) / BN;
+    int stages = (d.smem - 2048) / ManyShape<BN>::kStageBytes;
+    p.stages = stages > 8 ? 8 : stages;
+    const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(tiles < d.sms ? tiles : d.sms));
+    cfg.blockDim = dim3(ManyShape<BN>::kThreads);
+    cfg.dynamicSmemBytes = (size_t)ManyShape<BN>::smem_bytes(p.stages);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    SQZ_F8_TRY(cudaLaunchKernelEx(&cfg, fp8_gemm_many_kernel<BN>, mw, ma, p), "fp8 product launch");
+    return SQZ_OK;
+}
+
+constexpr int kFewRows = 128;  // up to here the few-row kernel, above it the many-row kernel
+
+sqz_status check_matrix(const sqz_fp8_matrix* x, const char* name, int64_t rows, int32_t k) {
+    if (!x) return host_fail(SQZ_ERR_INVALID_ARG, "%s is NULL", name);
+    if (x->format != SQZ_FP8_E4M3 && x->format != SQZ_FP8_E5M2)
+        return host_fail(SQZ_ERR_INVALID_ARG, "%s: unknown 8-bit format %d", name, x->format);
+    if (rows == 0 || k == 0) return SQZ_OK;
+    if (!x->q || !x->scale) return host_fail(SQZ_ERR_INVALID_ARG, "%s: codes or scales are NULL", name);
+    if (x->ld < k) return host_fail(SQZ_ERR_INVALID_ARG, "%s: ld=%lld < k=%d", name, (long long)x->ld, k);
+    if (x->ld_scale < (k + 127) / 128)
+        return host_fail(SQZ_ERR_INVALID_ARG, "%s: ld_scale=%lld < %d blocks", name, (long long)x->ld_scale,
+                         (k + 127) / 128);
+    if (!aligned16(x->q, x->ld))
+        return host_fail(SQZ_ERR_INVALID_ARG, "%s: codes must start on a 16-byte boundary with a pitch (ld) that is a "
+                                              "multiple of 16", name);
+    if (x->ld >= (int64_t)1 << 40) return host_fail(SQZ_ERR_INVALID_ARG, "%s: ld too large", name);
+    if (reinterpret_cast<uintptr_t>(x->scale) % 4)
+        return host_fail(SQZ_ERR_INVALID_ARG, "%s: scales must be 4-byte aligned", name);
+    return SQZ_OK;
+}
+
+}  // namespace
+
+extern "C" SQZ_API sqz_status sqz_fp8_quantize(const void* x, int32_t x_type, int64_t batch, int32_t rows,
+                                               int32_t cols, int64_t ldx, int32_t block_rows, int32_t format,
+                                               uint8_t* q, int64_t ldq, float* scale, int64_t ld_scale, void* stream) {
+    if (x_type != SQZ_TYPE_F16 && x_type != SQZ_TYPE_BF16)
+        return host_fail(SQZ_ERR_INVALID_ARG, "x_type=%d: fp16 or bf16 expected", x_type);
+    if (format != SQZ_FP8_E4M3 && format != SQZ_FP8_E5M2)
+        return host_fail(SQZ_ERR_INVALID_ARG, "unknown 8-bit format %d", format);
+    if (block_rows != 1 && block_rows != 128)
+        return host_fail(SQZ_ERR_INVALID_ARG, "block_rows=%d: 1 or 128 expected", block_rows);
+    if (batch < 0 || rows < 0 || cols < 0)
+        return host_fail(SQZ_ERR_INVALID_ARG, "negative size (batch=%lld, rows=%d, cols=%d)", (long long)batch, rows,
+                         cols);
+    if (rows > INT32_MAX - 127 || cols > INT32_MAX - 127) return host_fail(SQZ_ERR_INVALID_ARG, "rows or cols too large");
+    if (batch == 0 || rows == 0 || cols == 0) return SQZ_OK;
+    if (!x || !q || !scale) return host_fail(SQZ_ERR_INVALID_ARG, "x, q or scale is NULL");
+    const int nblocks = (cols + 127) / 128;
+    if (ldx < cols || ldq < cols || ld_scale < nblocks)
+        return host_fail(SQZ_ERR_INVALID_ARG, "ldx=%lld, ldq=%lld or ld_scale=%lld too small for %d columns",
+                         (long long)ldx, (long long)ldq, (long long)ld_scale, cols);
+    if (!aligned16(q, ldq))
+        return host_fail(SQZ_ERR_INVALID_ARG, "q must start on a 16-byte boundary with a pitch (ldq) that is a multiple "
+                                              "of 16");
+    if (reinterpret_cast<uintptr_t>(x) % 2 || reinterpret_cast<uintptr_t>(scale) % 4)
+        return host_fail(SQZ_ERR_INVALID_ARG, "x must be 2-byte and scale 4-byte aligned");
+    if (batch > (int64_t)1 << 31 || (block_rows == 128 && batch * ((rows + 127) / 128) > 65535) ||
+        batch * rows > ((int64_t)1 << 62) / nblocks)
+        return host_fail(SQZ_ERR_UNSUPPORTED, "too many row blocks (at most 65535 of 128 rows in one call)");
+    DeviceSizes d;
+    const sqz_status st = device_sizes(&d);
+    if (st != SQZ_OK) return st;
+    QuantParams p{};
+    p.x = static_cast<const uint16_t*>(x);
+    p.ldx = ldx;
+    p.q = q;
+    p.ldq = ldq;
+    p.scale = scale;
+    p.lds = ld_scale;
+    p.batch = batch;
+    p.rows = rows;
+    p.cols = cols;
+    p.nblocks = nblocks;
+    const bool vec = reinterpret_cast<uintptr_t>(x) % 16 == 0 && ldx % 8 == 0;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    cudaError_t e;
+    const int kind = (x_type == SQZ_TYPE_BF16 ? 4 : 0) | (format == SQZ_FP8_E5M2 ? 2 : 0) | (vec ? 1 : 0);
+    switch (kind) {
+        case 0: e = launch_quantize<false, false, false>(p, block_rows, d.sms, s); break;
+        case 1: e = launch_quantize<false, false, true>(p, block_rows, d.sms, s); break;
+        case 2: e = launch_quantize<false, true, false>(p, block_rows, d.sms, s); break;
+        case 3: e = launch_quantize<false, true, true>(p, block_rows, d.sms, s); break;
+        case 4: e = launch_quantize<true, false, false>(p, block_rows, d.sms, s); break;
+        case 5: e = launch_quantize<true, false, true>(p, block_rows, d.sms, s); break;
+        case 6: e = launch_quantize<true, true, false>(p, block_rows, d.sms, s); break;
+        default: e = launch_quantize<true, true, true>(p, block_rows, d.sms, s); break;
+    }
+    SQZ_F8_TRY(e, "fp8 quantize launch");
+    return SQZ_OK;
+}
+
+extern "C" SQZ_API sqz_status sqz_fp8_gemm(const sqz_fp8_matrix* a, const sqz_fp8_matrix* w, int32_t m, int32_t n,
+                                           int32_t k, void* y, int64_t ldy, int32_t y_type, void* stream) {
+    if (m < 0 || n < 0 || k < 0) return host_fail(SQZ_ERR_INVALID_ARG, "negative size (m=%d, n=%d, k=%d)", m, n, k);
+    if (m > INT32_MAX - 256 || n > INT32_MAX - 256 || k > INT32_MAX - 256)
+        return host_fail(SQZ_ERR_INVALID_ARG, "size too large (m=%d, n=%d, k=%d)", m, n, k);
+    if (y_type != SQZ_TYPE_F16 && y_type != SQZ_TYPE_BF16 && y_type != SQZ_TYPE_F32)
+        return host_fail(SQZ_ERR_INVALID_ARG, "unknown y_type %d", y_type);
+    sqz_status st = check_matrix(a, "a", m, k);
+    if (st != SQZ_OK) return st;
+    if ((st = check_matrix(w, "w", n, k)) != SQZ_OK) return st;
+    if (m == 0 || n == 0) return SQZ_OK;
+    if (!y) return host_fail(SQZ_ERR_INVALID_ARG, "y is NULL");
+    if (ldy < n) return host_fail(SQZ_ERR_INVALID_ARG, "ldy=%lld < n=%d", (long long)ldy, n);
+    const int out_bytes = y_type == SQZ_TYPE_F32 ? 4 : 2;
+    if (reinterpret_cast<uintptr_t>(y) % out_bytes) return host_fail(SQZ_ERR_INVALID_ARG, "y is not aligned to its type");
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (k == 0) {  // an empty sum (+0 is all-zero bits in every output type)
+        SQZ_F8_TRY(cudaMemset2DAsync(y, (size_t)ldy * out_bytes, 0, (size_t)n * out_bytes, (size_t)m, s), "clearing y");
+        return SQZ_OK;
+    }
+    DeviceSizes d;
+    if ((st = device_sizes(&d)) != SQZ_OK) return st;
+    GemmParams p{};
+    p.sa = a->scale;
+    p.ld_sa = a->ld_scale;
+    p.sw = w->scale;
+    p.ld_sw = w->ld_scale;
+    p.y = y;
+    p.ldy = ldy;
+    p.m = m;
+    p.n = n;
+    p.nkb = (k + 127) / 128;
+    p.out_type = y_type;
+    p.vec_out = reinterpret_cast<uintptr_t>(y) % 16 == 0 && ldy * out_bytes % 16 == 0;
+    if ((st = status_word(&p.status)) != SQZ_OK) return st;
+    CUtensorMap mw, ma;
+    const int64_t row_blocks = ((int64_t)n + 127) / 128;
+    if (m <= kFewRows && row_blocks <= 65535) {
+        const int tb = round_pow2(m);
+        if ((st = tile_map(&mw, w->q, k, n, w->ld, 128)) != SQZ_OK) return st;
+        if ((st = tile_map(&ma, a->q, k, m, a->ld, tb)) != SQZ_OK) return st;
+        p.idesc = instr_desc(w->format, a->format, 128, tb);
+        // K split over up to 8 CTAs of a cluster until the grid fills the SMs
+        int splits = 1;
+        while (splits < 8 && 2 * splits <= p.nkb && row_blocks * splits * 2 <= 2 * d.sms) splits *= 2;
+        const int per_cta = (p.nkb + splits - 1) / splits;
+        const int stage = tb * 128 + 16384 + (tb + 4) * 4;
+        int stages = (d.smem / 2 - 4096) / stage;  // two CTAs share an SM
+        if (stages > kMaxStages) stages = kMaxStages;
+        if (stages > per_cta) stages = per_cta;
+        if (stages < 1 || (int64_t)stages * (16384 + tb * 128) < (int64_t)tb * 512) stages = (tb * 512) / (16384 + tb * 128) + 1;
+        switch (tb) {
+            case 16: return launch_few<16>(mw, ma, p, splits, stages, d, s);
+            case 32: return launch_few<32>(mw, ma, p, splits, stages, d, s);
+            case 64: return launch_few<64>(mw, ma, p, splits, stages, d, s);
+            default: return launch_few<128>(mw, ma, p, splits, stages, d, s);
+        }
+    }
+    // The widest tile costs least per output; narrower ones when they need
+    // fewer rounds of the SMs (weights: measured time of a tile's block of K).
+    const int64_t tm = (m + 127) / 128;
+    const auto rounds = [&](int bn, double weight) {
+        const int64_t tiles = tm * (((int64_t)n + bn - 1) / bn);
+        return (double)((tiles + d.sms - 1) / d.sms) * weight;
+    };
+    const double c256 = rounds(256, 1.0), c128 = rounds(128, 0.55), c64 = rounds(64, 0.4);
+    const int bn = c256 <= c128 && c256 <= c64 ? 256 : c128 <= c64 ? 128 : 64;
+    if ((st = tile_map(&mw, w->q, k, n, w->ld, bn)) != SQZ_OK) return st;
+    if ((st = tile_map(&ma, a->q, k, m, a->ld, 128)) != SQZ_OK) return st;
+    p.idesc = instr_desc(a->format, w->format, 128, bn);
+    switch (bn) {
+        case 256: return launch_many<256>(mw, ma, p, d, s);
+        case 128: return launch_many<128>(mw, ma, p, d, s);
+        default: return launch_many<64>(mw, ma, p, d, s);
+    }
+}
+
+extern "C" SQZ_API sqz_status sqz_fp8_status(void* stream, int32_t* status) {
+    if (!status) return host_fail(SQZ_ERR_INVALID_ARG, "status is NULL");
+    *status = 0;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+    SQZ_F8_TRY(cudaStreamIsCapturing(s, &cap), "cudaStreamIsCapturing");
+    if (cap != cudaStreamCaptureStatusNone)
+        return host_fail(SQZ_ERR_UNSUPPORTED, "the stream is being captured into a CUDA graph; reading the status "
+                                              "synchronises, which a capture cannot contain");
+    int* word = nullptr;
+    const sqz_status st = status_word(&word);
+    if (st != SQZ_OK) return st;
+    int h = 0;
+    SQZ_F8_TRY(cudaMemcpyAsync(&h, word, sizeof h, cudaMemcpyDeviceToHost, s), "reading the status");
+    SQZ_F8_TRY(cudaMemsetAsync(word, 0, sizeof h, s), "clearing the status");
+    SQZ_F8_TRY(cudaStreamSynchronize(s), "reading the status");
+    *status = h;
+    if (h & 1)
+        return host_fail(SQZ_ERR_TIMEOUT, "a bounded device wait gave up (status 0x%x): y of the affected call is "
+                                          "undefined", h);
+    return SQZ_OK;
+}

@@ -1,0 +1,293 @@
+"""GPU tests of the block-scaled 8-bit quantizer and matrix product against
+their definitions.
+
+Quantizer: the definition is exact (one fp32 division per scale and per
+element, one rounding to 8 bits), so codes and scales are compared bit for bit
+with the same steps done by torch on the CPU.
+
+Product: compared with the fp64 sum.  Bound per output, S = sum |a w| (scaled):
+the result's rounding, half a step of y's type relative to y; the tensor
+cores' sum of 128 exact products, at most one fp32 step (2^-23) of S per
+addition, 128 * 2^-23 S; the blocks' scale products and additions in fp32,
+(blocks + 3) * 2^-24 S.  fp16 results below 2^-14 are rounded to a step of
+2^-24.
+"""
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+E4M3, E5M2 = torch.float8_e4m3fn, torch.float8_e5m2
+LARGEST = {E4M3: 448.0, E5M2: 57344.0}
+
+
+@pytest.fixture(scope="module")
+def B():
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    from lut_dequant_gemv_b200 import binding, build
+
+    build.build()
+    binding.lib()
+    return binding
+
+
+def quantize_ref(x, block_rows, dtype):
+    """The definition on the CPU in fp32: x [batch, rows, cols]."""
+    z, r, c = x.shape
+    p = torch.nn.functional.pad(x.float(), (0, -c % 128, 0, -r % block_rows))
+    p = p.view(z, p.shape[1] // block_rows, block_rows, p.shape[2] // 128, 128)
+    big = p.abs().amax(dim=(2, 4))
+    scale = torch.where(big == 0, torch.ones_like(big), big / LARGEST[dtype])
+    v = (p / scale[:, :, None, :, None]).clamp(-LARGEST[dtype], LARGEST[dtype])
+    q = v.view(z, -1, p.shape[3] * 128)[:, :r, :c].contiguous().to(dtype)
+    return q, scale
+
+
+def same_codes(a, b):
+    a, b = a.contiguous().view(torch.uint8), b.contiguous().view(torch.uint8)
+    return torch.equal(a, b)
+
+
+def make_x(gen, shape, dtype, kind="normal"):
+    x = torch.randn(shape, generator=gen)
+    if kind == "wide":  # values over many binades, zeros among them
+        x = x * torch.exp2(torch.randint(-20, 8, shape, generator=gen).float())
+        x[torch.rand(shape, generator=gen) < 0.2] = 0
+    return x.to(dtype)
+
+
+@pytest.mark.parametrize("fmt", [E4M3, E5M2])
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("batch,rows,cols,block_rows", [
+    (1, 1, 1, 1), (1, 1, 4096, 1), (1, 3, 127, 1), (1, 5, 129, 1), (2, 7, 1000, 1), (1, 300, 777, 1),
+    (1, 1, 1, 128), (1, 128, 128, 128), (1, 129, 255, 128), (3, 200, 300, 128), (2, 127, 1024, 128),
+])
+def test_quantize_is_the_definition(B, fmt, dtype, batch, rows, cols, block_rows):
+    gen = torch.Generator().manual_seed(rows * 1000 + cols)
+    for kind in ("normal", "wide"):
+        x = make_x(gen, (batch, rows, cols), dtype, kind)
+        q, s = B.sqz_fp8_quantize(x.cuda(), block_rows, fmt)
+        q_ref, s_ref = quantize_ref(x, block_rows, fmt)
+        assert torch.equal(s.cpu(), s_ref)
+        assert same_codes(q.cpu(), q_ref)
+
+
+def test_quantize_division_is_correctly_rounded(B):
+    """Every quotient, over blocks whose scales span fp16's and bf16's range (the three-step quotient and, at
+    the ends of the range, the division)."""
+    gen = torch.Generator().manual_seed(5)
+    for dtype, lo, hi in ((torch.float16, -22, 14), (torch.bfloat16, -130, 125)):
+        e = torch.randint(lo, hi, (4096, 1), generator=gen).float()
+        x = ((torch.rand((4096, 256), generator=gen) * 2 - 1) * torch.exp2(e)).to(dtype)
+        q, s = B.sqz_fp8_quantize(x.cuda(), 1, E4M3)
+        q_ref, s_ref = quantize_ref(x[None], 1, E4M3)
+        assert torch.equal(s.cpu(), s_ref[0])
+        assert same_codes(q.cpu(), q_ref[0])
+
+
+def test_quantize_strides_alignment_and_edges(B):
+    """x at every alignment and pitch; the codes' pitch padding and the scales' padding stay as they were."""
+    gen = torch.Generator().manual_seed(6)
+    for off, ldx in ((0, 200), (1, 201), (3, 240), (8, 208)):
+        big = make_x(gen, (40 * 256,), torch.float16).cuda()
+        x = big[off:off + 40 * ldx].view(40, ldx)[:, :193]
+        qb = torch.full((40, 224), 7, dtype=torch.uint8, device="cuda").view(E4M3)
+        sb = torch.full((40, 5), -1.0, device="cuda")
+        B.sqz_fp8_quantize(x, 1, q=qb[:, :193], scale=sb[:, :2])
+        q_ref, s_ref = quantize_ref(x.cpu()[None], 1, E4M3)
+        assert same_codes(qb[:, :193].cpu(), q_ref[0]) and torch.equal(sb[:, :2].cpu(), s_ref[0])
+        assert bool((qb.view(torch.uint8)[:, 193:] == 7).all()) and bool((sb[:, 2:] == -1).all())
+
+
+def test_quantize_zeros_infinities_and_nan(B):
+    x = torch.randn(6, 256).half()
+    x[0] = 0
+    x[1, 3] = float("inf")
+    x[2, 130] = float("nan")
+    x[3, 5], x[3, 6] = float("-inf"), float("nan")
+    x[4] = -0.0
+    x[5] = torch.finfo(torch.float16).smallest_normal / 1024  # the smallest subnormal
+    q, s = B.sqz_fp8_quantize(x.cuda())
+    v, s = q.cpu().float(), s.cpu()
+    assert torch.equal(s[0], torch.ones(2)) and bool((v[0] == 0).all()) and bool((v[4] == 0).all())
+    assert s[1, 0] == float("inf") and bool(v[1, 3].isnan()) and bool((v[1, :3] == 0).all())
+    assert bool(s[2, 1].isnan()) and bool(v[2, 128:].isnan().all()) and not bool(v[2, :128].isnan().any())
+    assert bool(s[3, 0].isnan()) and bool(v[3, :128].isnan().all())
+    assert bool((v[5] == 448).all())
+
+
+def random_matrix(gen, rows, k, fmt, block_rows, pitch_extra=0):
+    spread = 100.0 if fmt == E4M3 else 10000.0
+    ld = (k + 15) // 16 * 16 + pitch_extra
+    # the bytes between k and the pitch are NaN codes: they must not be read
+    q = torch.full((rows, ld), 0x7F, dtype=torch.uint8).view(fmt)
+    q[:, :k] = (torch.randn((rows, k), generator=gen) * spread).clamp(-4 * spread, 4 * spread).to(fmt)
+    s = (0.5 + torch.rand((-(-rows // block_rows), -(-k // 128)), generator=gen)) / spread
+    q = q.cuda()[:, :k]
+    return q, s.cuda()
+
+
+def dense(q, s, block_rows):
+    full = s.double().repeat_interleave(block_rows, 0)[: q.shape[0]].repeat_interleave(128, 1)[:, : q.shape[1]]
+    return q.double() * full
+
+
+def check_product(y, a, sa, w, sw):
+    A, W = dense(a, sa, 1), dense(w, sw, 128)
+    ref, S = A @ W.t(), A.abs() @ W.abs().t()
+    blocks = sa.shape[1]
+    fi = torch.finfo(y.dtype)
+    tol = fi.eps / 2 * ref.abs() + (2.0 ** -16 + (blocks + 3) * 2.0 ** -24) * S * (1 + fi.eps)
+    if y.dtype == torch.float16:
+        tol = tol + 2.0 ** -25
+    err = (y.double() - ref).abs()
+    bad = ~(err <= tol)
+    assert not bool(bad.any()), (int(bad.sum()), bad.nonzero()[:4].tolist(), float((err / tol).max()))
+
+
+SIZES = [
+    (1, 1, 1), (1, 8, 16), (1, 128, 128), (1, 4096, 4096), (2, 300, 1000), (16, 129, 513), (17, 128, 2048),
+    (33, 1000, 300), (64, 640, 1152), (65, 200, 4100), (128, 257, 129), (129, 300, 130), (200, 64, 640),
+    (257, 1111, 272), (500, 2050, 1000), (1000, 2048, 128), (300, 40, 5000),
+]
+
+
+@pytest.mark.parametrize("m,n,k", SIZES)
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16, torch.float32])
+def test_product_sizes_and_types(B, m, n, k, dtype):
+    gen = torch.Generator().manual_seed(m * 7 + n * 3 + k)
+    a, sa = random_matrix(gen, m, k, E4M3, 1)
+    w, sw = random_matrix(gen, n, k, E4M3, 128, pitch_extra=16 if n % 2 else 0)
+    y = torch.full((m, n), float("nan"), dtype=dtype, device="cuda")
+    B.sqz_fp8_gemm(a, sa, w, sw, y)
+    check_product(y, a, sa, w, sw)
+    assert B.sqz_fp8_status() == 0
+
+
+@pytest.mark.parametrize("fa", [E4M3, E5M2])
+@pytest.mark.parametrize("fw", [E4M3, E5M2])
+@pytest.mark.parametrize("m", [5, 300])
+def test_product_formats(B, fa, fw, m):
+    gen = torch.Generator().manual_seed(11)
+    a, sa = random_matrix(gen, m, 700, fa, 1)
+    w, sw = random_matrix(gen, 390, 700, fw, 128)
+    y = torch.empty((m, 390), device="cuda")
+    B.sqz_fp8_gemm(a, sa, w, sw, y)
+    check_product(y, a, sa, w, sw)
+
+
+@pytest.mark.parametrize("m", [3, 40, 150, 400])
+@pytest.mark.parametrize("dtype", [torch.float16, torch.float32])
+def test_product_strides(B, m, dtype):
+    """Pitches beyond the sizes, an unaligned y; what lies behind y's columns and last row stays."""
+    gen = torch.Generator().manual_seed(12)
+    n, k = 333, 400
+    a, sa = random_matrix(gen, m, k, E4M3, 1, pitch_extra=48)
+    w, sw = random_matrix(gen, n, k, E4M3, 128, pitch_extra=32)
+    sa_wide = torch.full((m, 9), float("nan"), device="cuda")
+    sa_wide[:, :4] = sa
+    for off, ldy in ((0, 336), (1, 341)):
+        buf = torch.full(((m + 2) * ldy + off,), -7.0, dtype=dtype, device="cuda")
+        y = buf[off:].view(m + 2, ldy)
+        B.sqz_fp8_gemm(a, sa_wide[:, :4], w, sw, y[:m, :n])
+        check_product(y[:m, :n], a, sa, w, sw)
+        assert bool((y[:m, n:] == -7).all()) and bool((y[m:] == -7).all()) and bool((buf[:off] == -7).all())
+
+
+def test_product_equals_itself_bit_for_bit(B):
+    gen = torch.Generator().manual_seed(13)
+    for m, n, k in ((1, 1000, 4096), (100, 500, 3000), (300, 700, 3000)):
+        a, sa = random_matrix(gen, m, k, E4M3, 1)
+        w, sw = random_matrix(gen, n, k, E4M3, 128)
+        ys = [torch.empty((m, n), device="cuda") for _ in range(3)]
+        for y in ys:
+            B.sqz_fp8_gemm(a, sa, w, sw, y)
+        assert torch.equal(ys[0], ys[1]) and torch.equal(ys[0], ys[2])
+
+
+@pytest.mark.parametrize("m", [4, 260])
+def test_product_with_nan_codes_and_scales(B, m):
+    gen = torch.Generator().manual_seed(14)
+    a, sa = random_matrix(gen, m, 384, E4M3, 1)
+    w, sw = random_matrix(gen, 200, 384, E4M3, 128)
+    a.view(torch.uint8)[2, 200] = 0x7F  # a NaN code: row 2
+    w.view(torch.uint8)[77, 5] = 0xFF   # column 77
+    sa[1, 0] = float("inf")             # row 1: infinite (or NaN) everywhere
+    y = torch.empty((m, 200), device="cuda")
+    B.sqz_fp8_gemm(a, sa, w, sw, y)
+    assert bool(y[2].isnan().all()) and bool(y[:, 77].isnan().all()) and not bool(y[1].isfinite().any())
+    keep = [r for r in range(m) if r not in (1, 2)]
+    cols = [c for c in range(200) if c != 77]
+    assert bool(y[keep][:, cols].isfinite().all())
+
+
+def test_product_of_empty_sizes(B):
+    f = dict(device="cuda")
+    y = torch.full((3, 5), 9.0, **f)
+    z = torch.empty((3, 0), dtype=E4M3, **f)
+    B.sqz_fp8_gemm(z, torch.empty((3, 0), **f), torch.empty((5, 0), dtype=E4M3, **f), torch.empty((1, 0), **f), y)
+    assert bool((y == 0).all())
+    a = torch.zeros((0, 128), dtype=E4M3, **f)
+    w = torch.zeros((5, 128), dtype=E4M3, **f)
+    B.sqz_fp8_gemm(a, torch.empty((0, 1), **f), w, torch.ones((1, 1), **f), torch.empty((0, 5), **f))
+
+
+@pytest.mark.parametrize("m", [2, 200])
+def test_on_another_stream_and_in_a_graph(B, m):
+    """Quantize then multiply on a side stream, and the pair captured and replayed on new inputs."""
+    gen = torch.Generator().manual_seed(15)
+    n, k = 512, 1024
+    xs = [torch.randn((m, k), generator=gen).bfloat16().cuda() for _ in range(3)]
+    w, sw = random_matrix(gen, n, k, E4M3, 128)
+    want = []
+    for x in xs:
+        q, s = B.sqz_fp8_quantize(x)
+        y = torch.empty((m, n), device="cuda")
+        B.sqz_fp8_gemm(q, s, w, sw, y)
+        check_product(y, q, s, w, sw)
+        want.append(y)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    x_in, y_out = torch.empty_like(xs[0]), torch.empty((m, n), device="cuda")
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        q, s = B.sqz_fp8_quantize(xs[0])
+        B.sqz_fp8_gemm(q, s, w, sw, y_out)
+    side.synchronize()
+    assert torch.equal(y_out, want[0])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        B.sqz_fp8_quantize(x_in, q=q, scale=s)
+        B.sqz_fp8_gemm(q, s, w, sw, y_out)
+    for x, y in zip(xs, want):
+        x_in.copy_(x)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y_out, y)
+
+
+def test_prompt_through_a_lut_layer(B, orc):
+    """A LUT layer's dense part, dequantized and requantized to 8 bits, for a prompt of more rows than sqz_gemv
+    takes; its first rows against sqz_gemv within the error of the two 8-bit roundings (each off by at most
+    half a step: 2^-4 of the value)."""
+    import numpy as np
+    import synth
+
+    L = synth.make_layer(300, 1024, 3, 0.0, seed=4, key="prompt")
+    layer = B.create_layer_from_numpy(L.n_out, L.k_in, L.bits, L.codes, L.lut, L.rowptr, L.col, L.val)
+    dense_w = torch.empty((300, 1024), dtype=torch.float16, device="cuda")
+    B.sqz_debug_dequant(layer, dense_w)
+    w, sw = B.sqz_fp8_quantize(dense_w, 128)
+    x = torch.from_numpy(synth.make_x(40, 1024, seed=1).view(np.float16).copy()).cuda()
+    a, sa = B.sqz_fp8_quantize(x)
+    y = torch.empty((40, 300), dtype=torch.float16, device="cuda")
+    B.sqz_fp8_gemm(a, sa, w, sw, y)
+    check_product(y, a, sa, w, sw)
+    y16 = torch.empty((16, 300), dtype=torch.float16, device="cuda")
+    B.sqz_gemv(layer, x[:16], y16)
+    bound = x[:16].double().abs() @ dense_w.double().abs().t()
+    # subnormal codes add an absolute error of half the smallest code (2^-10) times the scale
+    slack = 2.0 ** -10 * (sa.double().repeat_interleave(128, 1)[:16] @ dense_w.double().abs().t()
+                          + x[:16].double().abs() @ sw.double().repeat_interleave(128, 0)[:300].repeat_interleave(128, 1).t())
+    assert bool(((y[:16].double() - y16.double()).abs() <= (2 * 2.0 ** -4 + 2.0 ** -7) * bound + 1.1 * slack).all())
+    layer.close()
