@@ -454,6 +454,94 @@ SQZ_API sqz_status sqz_fp8_gemm(const sqz_fp8_matrix* a, const sqz_fp8_matrix* w
  */
 SQZ_API sqz_status sqz_fp8_status(void* stream, int32_t* status);
 
+/* ------------------------------------------------ mixture of experts ---
+ * A whole mixture-of-experts layer for a few tokens in one kernel launch:
+ *
+ *     l = x R^T, p = softmax(l) over the experts,
+ *     the top_k experts of each token by l (equal logits: the lower index),
+ *     g = p of those experts (renormalize: divided by their sum),
+ *     h_e = silu(W1_e x) * (W3_e x), silu(v) = v / (1 + exp(-v)),
+ *     y = sum over the chosen e of g_e W2_e h_e
+ *
+ * with W1 (gate), W3 (up) and W2 (down) in 8 bits (SQZ_FP8_E4M3) with one
+ * fp32 scale per 128 x 128 block, as sqz_fp8_quantize makes them.
+ */
+#define SQZ_MOE_MAX_TOKENS 32
+#define SQZ_MOE_MAX_EXPERTS 1024
+#define SQZ_MOE_MAX_TOP_K 16
+
+typedef struct sqz_moe* sqz_moe_t;
+
+/* All pointers are device pointers on the current device.  The arrays are
+ * borrowed, not copied (the experts of a layer are gigabytes): they stay
+ * alive and unchanged as long as the handle is used. */
+typedef struct {
+    int32_t experts;        /* 1 .. SQZ_MOE_MAX_EXPERTS                                     */
+    int32_t top_k;          /* 1 .. min(SQZ_MOE_MAX_TOP_K, experts)                         */
+    int32_t hidden;         /* size of x and y, a multiple of 16                            */
+    int32_t inter;          /* inner size of an expert, a multiple of 16                    */
+    int32_t x_type;         /* SQZ_TYPE_F16 or SQZ_TYPE_BF16: x, y and the router           */
+    int32_t renormalize;    /* 1: the chosen experts' weights sum to 1                      */
+    const void* router;     /* [experts][ld_router]                                         */
+    int64_t ld_router;      /* >= hidden                                                    */
+    const uint8_t* w13;     /* [experts][2][inter][hidden] codes: gate rows, then up rows   */
+    const float* w13_scale; /* [experts][2][ceil(inter/128)][ceil(hidden/128)]              */
+    const uint8_t* w2;      /* [experts][hidden][inter] codes                               */
+    const float* w2_scale;  /* [experts][ceil(hidden/128)][ceil(inter/128)]                 */
+} sqz_moe_desc;
+
+/*
+ * Make a handle (host data only).  Errors: SQZ_ERR_INVALID_ARG for NULL
+ * pointers, sizes outside the ranges above, codes not on a 16-byte boundary;
+ * SQZ_ERR_UNSUPPORTED for 2^31 or more weight blocks; SQZ_ERR_OOM;
+ * SQZ_ERR_CUDA.  On error *out is NULL.
+ */
+SQZ_API sqz_status sqz_create_moe(const sqz_moe_desc* desc, sqz_moe_t* out);
+
+/* Bytes of device workspace a call of up to `tokens` tokens needs. */
+SQZ_API sqz_status sqz_moe_workspace_bytes(sqz_moe_t moe, int32_t tokens, int64_t* bytes);
+
+/*
+ * y [tokens][ldy] = the layer applied to x [tokens][ldx], asynchronously on
+ * `stream`, on the device the handle was made on.  ids [tokens][top_k] and
+ * weights [tokens][top_k] (either may be NULL) receive the chosen experts, in
+ * the order of falling logits, and their g.
+ *
+ * workspace: device memory on a 256-byte boundary of at least
+ * sqz_moe_workspace_bytes(moe, tokens) bytes, zeroed once before its first
+ * use with this handle; each call leaves it ready for the next, of any number
+ * of tokens that fits.  Calls that share a workspace must not overlap (the
+ * same stream, or ordered by events); calls with workspaces of their own may.
+ * The launch is cooperative, one CTA on every SM, and may be captured into a
+ * graph (which then owns its workspace while it runs).
+ *
+ * Arithmetic: the codes' products are exact; x and h enter the tensor cores
+ * as four 8-bit digits each, which represent x exactly (values below 2^-10 of
+ * the largest of their block of 128 within 2^-29 of it) and h to 2^-19; sums are
+ * in fp32; y is rounded once.  Bitwise reproducible.  A token whose x or h is
+ * not finite, or whose logits hold a NaN, gets NaN; its ids stay in range.
+ *
+ * Errors: SQZ_ERR_INVALID_ARG (NULL, tokens outside [0, SQZ_MOE_MAX_TOKENS],
+ * pitches below hidden, a small or misaligned workspace, another device);
+ * SQZ_ERR_CUDA.  No synchronisation.
+ */
+SQZ_API sqz_status sqz_moe_forward(sqz_moe_t moe, const void* x, int32_t tokens, int64_t ldx, void* y, int64_t ldy,
+                                   int32_t* ids, float* weights, void* workspace, int64_t workspace_bytes,
+                                   void* stream);
+
+/*
+ * Read a workspace's status word, ordered on `stream` (synchronises it;
+ * refused with SQZ_ERR_UNSUPPORTED on a stream under capture).  0: every call
+ * completed normally; bit 0 (1): a bounded wait gave up, y of that call is
+ * undefined and the workspace has to be zeroed before its next use (returns
+ * SQZ_ERR_TIMEOUT with *status set).
+ */
+SQZ_API sqz_status sqz_moe_status(void* workspace, void* stream, int32_t* status);
+
+/* Release a handle.  NULL is accepted.  The caller must make sure no work
+ * that uses the handle is still in flight. */
+SQZ_API sqz_status sqz_destroy_moe(sqz_moe_t moe);
+
 /* Message for the calling thread's last non-OK status ("" if none). */
 SQZ_API const char* sqz_last_error(void);
 

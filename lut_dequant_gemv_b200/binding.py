@@ -36,6 +36,9 @@ SQZ_FP8_E5M2 = 1
 SQZ_TYPE_F16 = 0
 SQZ_TYPE_BF16 = 1
 SQZ_TYPE_F32 = 2
+SQZ_MOE_MAX_TOKENS = 32
+SQZ_MOE_MAX_EXPERTS = 1024
+SQZ_MOE_MAX_TOP_K = 16
 
 STATUS_NAMES = {0: "SQZ_OK", 1: "SQZ_ERR_INVALID_ARG", 2: "SQZ_ERR_UNSUPPORTED", 3: "SQZ_ERR_CUDA",
                 4: "SQZ_ERR_OOM", 5: "SQZ_ERR_TIMEOUT"}
@@ -45,7 +48,8 @@ EXPORTED = ("sqz_create_layer", "sqz_gemv", "sqz_gemv_host", "sqz_debug_dequant"
             "sqz_destroy", "sqz_fp16_gemv", "sqz_last_error", "sqz_version", "sqz_check_csr_static",
             "sqz_layer_set_mac", "sqz_layer_set_csr_mode", "sqz_layer_status", "sqz_encode",
             "sqz_encode_outliers", "sqz_plan_query", "sqz_layer_set_predecode", "sqz_tile_split_query",
-            "sqz_fp8_quantize", "sqz_fp8_gemm", "sqz_fp8_status")
+            "sqz_fp8_quantize", "sqz_fp8_gemm", "sqz_fp8_status", "sqz_create_moe", "sqz_moe_workspace_bytes",
+            "sqz_moe_forward", "sqz_moe_status", "sqz_destroy_moe")
 
 
 class SqzError(RuntimeError):
@@ -81,6 +85,17 @@ class sqz_fp8_matrix(ctypes.Structure):
         ("scale", ctypes.c_void_p),
         ("ld_scale", ctypes.c_int64),
         ("format", ctypes.c_int32),
+    ]
+
+
+class sqz_moe_desc(ctypes.Structure):
+    _fields_ = [(name, ctypes.c_int32) for name in ("experts", "top_k", "hidden", "inter", "x_type", "renormalize")] + [
+        ("router", ctypes.c_void_p),
+        ("ld_router", ctypes.c_int64),
+        ("w13", ctypes.c_void_p),
+        ("w13_scale", ctypes.c_void_p),
+        ("w2", ctypes.c_void_p),
+        ("w2_scale", ctypes.c_void_p),
     ]
 
 
@@ -130,6 +145,14 @@ def lib() -> ctypes.CDLL:
         L.sqz_fp8_gemm.restype = ctypes.c_int
         L.sqz_fp8_status.argtypes = [P, ctypes.POINTER(i32)]
         L.sqz_fp8_status.restype = ctypes.c_int
+        L.sqz_create_moe.argtypes = [ctypes.POINTER(sqz_moe_desc), ctypes.POINTER(P)]
+        L.sqz_moe_workspace_bytes.argtypes = [P, i32, ctypes.POINTER(i64)]
+        L.sqz_moe_forward.argtypes = [P, P, i32, i64, P, i64, P, P, P, i64, P]
+        L.sqz_moe_status.argtypes = [P, P, ctypes.POINTER(i32)]
+        L.sqz_destroy_moe.argtypes = [P]
+        for name in ("sqz_create_moe", "sqz_moe_workspace_bytes", "sqz_moe_forward", "sqz_moe_status",
+                     "sqz_destroy_moe"):
+            getattr(L, name).restype = ctypes.c_int
         L.sqz_encode_outliers.argtypes = [i64, ctypes.c_double]
         L.sqz_encode_outliers.restype = i64
         L.sqz_last_error.argtypes = []
@@ -410,6 +433,7 @@ def sqz_layer_status(layer: Layer, stream=None) -> int:
 
 # ------------------------------------------------ 8-bit floating point, block scales
 _FP8_FORMATS = {torch.float8_e4m3fn: SQZ_FP8_E4M3, torch.float8_e5m2: SQZ_FP8_E5M2}
+_H16_TYPES = (torch.float16, torch.bfloat16)
 _TYPES = {torch.float16: SQZ_TYPE_F16, torch.bfloat16: SQZ_TYPE_BF16, torch.float32: SQZ_TYPE_F32}
 
 
@@ -449,7 +473,7 @@ def sqz_fp8_quantize(x: torch.Tensor, block_rows: int = 1, dtype: torch.dtype = 
     if x.dim() not in (2, 3):
         raise ValueError("x must be [rows, cols] or [batch, rows, cols]")
     _on_current_device(x, "x")
-    if x.dtype not in _TYPES or x.dtype == torch.float32:
+    if x.dtype not in _H16_TYPES:
         raise TypeError(f"x has dtype {x.dtype}, expected fp16 or bf16")
     if block_rows not in (1, 128):
         raise ValueError("block_rows must be 1 or 128")
@@ -512,3 +536,118 @@ def sqz_fp8_status(stream=None) -> int:
     st = ctypes.c_int32(-1)
     _check(lib().sqz_fp8_status(_stream(stream), ctypes.byref(st)), "sqz_fp8_status")
     return int(st.value)
+
+
+# ------------------------------------------------ mixture of experts
+class Moe:
+    """Owning handle for an ``sqz_moe_t`` (destroyed on garbage collection); keeps the borrowed weights alive."""
+
+    def __init__(self, handle: int, desc: sqz_moe_desc, dtype: torch.dtype, tensors):
+        self.handle = ctypes.c_void_p(handle)
+        self.experts, self.top_k, self.hidden, self.inter = desc.experts, desc.top_k, desc.hidden, desc.inter
+        self.dtype, self._tensors = dtype, tensors
+
+    def close(self) -> None:
+        if self.handle is not None and self.handle.value:
+            sqz_destroy_moe(self)
+        self.handle = self._tensors = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    @property
+    def _as_parameter_(self):
+        if self.handle is None:
+            raise ValueError("moe has been destroyed")
+        return self.handle
+
+
+def sqz_create_moe(router: torch.Tensor, w13: torch.Tensor, w13_scale: torch.Tensor, w2: torch.Tensor,
+                   w2_scale: torch.Tensor, top_k: int, renormalize: bool = True) -> Moe:
+    """A mixture-of-experts layer: router [experts, hidden] (fp16 or bf16, also x's and y's type), w13
+    [experts, 2 * inter, hidden] (gate rows, then up rows) and w2 [experts, hidden, inter] float8_e4m3fn, their fp32
+    scales [experts, 2, ceil(inter/128), ceil(hidden/128)] and [experts, ceil(hidden/128), ceil(inter/128)].  The
+    tensors are borrowed."""
+    for name, t in (("router", router), ("w13", w13), ("w13_scale", w13_scale), ("w2", w2), ("w2_scale", w2_scale)):
+        _on_current_device(t, name)
+        if name != "router" and not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+    if router.dim() != 2 or w13.dim() != 3 or w2.dim() != 3:
+        raise ValueError("router must be 2-D, w13 and w2 3-D")
+    if router.dtype not in _H16_TYPES:
+        raise TypeError(f"router has dtype {router.dtype}, expected fp16 or bf16")
+    if w13.dtype != torch.float8_e4m3fn or w2.dtype != torch.float8_e4m3fn:
+        raise TypeError("w13 and w2 must be float8_e4m3fn")
+    if w13_scale.dtype != torch.float32 or w2_scale.dtype != torch.float32:
+        raise TypeError("the scales must be fp32")
+    (experts, hidden), inter = router.shape, w2.shape[2]
+    bi, bh = -(-inter // 128), -(-hidden // 128)
+    if w13.shape != (experts, 2 * inter, hidden) or w2.shape != (experts, hidden, inter) or \
+            w13_scale.shape != (experts, 2, bi, bh) or w2_scale.shape != (experts, bh, bi):
+        raise ValueError(f"shapes do not fit together: router {tuple(router.shape)}, w13 {tuple(w13.shape)}, w13_scale "
+                         f"{tuple(w13_scale.shape)}, w2 {tuple(w2.shape)}, w2_scale {tuple(w2_scale.shape)}")
+    if router.stride(1) != 1:
+        raise ValueError("router must be row-major")
+    d = sqz_moe_desc(experts=experts, top_k=top_k, hidden=hidden, inter=inter, x_type=_TYPES[router.dtype],
+                     renormalize=int(renormalize), router=router.data_ptr(),
+                     ld_router=router.stride(0) if experts > 1 else hidden, w13=w13.data_ptr(),
+                     w13_scale=w13_scale.data_ptr(), w2=w2.data_ptr(), w2_scale=w2_scale.data_ptr())
+    out = ctypes.c_void_p()
+    _check(lib().sqz_create_moe(ctypes.byref(d), ctypes.byref(out)), "sqz_create_moe")
+    return Moe(out.value, d, router.dtype, (router, w13, w13_scale, w2, w2_scale))
+
+
+def sqz_moe_workspace_bytes(moe: Moe, tokens: int) -> int:
+    n = ctypes.c_int64(0)
+    _check(lib().sqz_moe_workspace_bytes(moe, int(tokens), ctypes.byref(n)), "sqz_moe_workspace_bytes")
+    return int(n.value)
+
+
+def sqz_moe_workspace(moe: Moe, tokens: int) -> torch.Tensor:
+    """A zeroed workspace for calls of up to `tokens` tokens, on the current device."""
+    return torch.zeros(sqz_moe_workspace_bytes(moe, tokens), dtype=torch.uint8, device="cuda")
+
+
+def sqz_moe_forward(moe: Moe, x: torch.Tensor, y: torch.Tensor, ids: Optional[torch.Tensor] = None,
+                    weights: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                    stream=None) -> None:
+    """y [tokens, hidden] = the layer applied to x; ids (int32) and weights (fp32) [tokens, top_k] receive the routing.
+    workspace: from sqz_moe_workspace, not shared with a call that may overlap."""
+    if workspace is None:
+        raise ValueError("workspace is required (sqz_moe_workspace)")
+    for name, t in (("x", x), ("y", y)):
+        _on_current_device(t, name)
+        if t.dtype != moe.dtype or t.dim() != 2 or t.shape[1] != moe.hidden or (t.stride(1) != 1 and moe.hidden > 1):
+            raise ValueError(f"{name} must be a row-major [tokens, {moe.hidden}] tensor of {moe.dtype}")
+    tokens = x.shape[0]
+    if y.shape[0] != tokens:
+        raise ValueError(f"x has {tokens} rows, y {y.shape[0]}")
+    for name, t, dt in (("ids", ids, torch.int32), ("weights", weights, torch.float32)):
+        if t is not None:
+            _on_current_device(t, name)
+            if t.dtype != dt or t.shape != (tokens, moe.top_k) or not t.is_contiguous():
+                raise ValueError(f"{name} must be a contiguous [{tokens}, {moe.top_k}] tensor of {dt}")
+    _on_current_device(workspace, "workspace")
+    if workspace.dtype != torch.uint8 or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous uint8 tensor")
+    one = tokens <= 1
+    _check(lib().sqz_moe_forward(moe, x.data_ptr(), tokens, moe.hidden if one else x.stride(0), y.data_ptr(),
+                                 moe.hidden if one else y.stride(0), None if ids is None else ids.data_ptr(),
+                                 None if weights is None else weights.data_ptr(), workspace.data_ptr(),
+                                 workspace.numel(), _stream(stream)), "sqz_moe_forward")
+
+
+def sqz_moe_status(workspace: torch.Tensor, stream=None) -> int:
+    _on_current_device(workspace, "workspace")
+    st = ctypes.c_int32(-1)
+    _check(lib().sqz_moe_status(workspace.data_ptr(), _stream(stream), ctypes.byref(st)), "sqz_moe_status")
+    return int(st.value)
+
+
+def sqz_destroy_moe(moe) -> None:
+    _check(lib().sqz_destroy_moe(moe.handle if isinstance(moe, Moe) else moe), "sqz_destroy_moe")
+    if isinstance(moe, Moe):
+        moe.handle = None

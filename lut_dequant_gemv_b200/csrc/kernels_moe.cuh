@@ -1,0 +1,755 @@
+// kernels_moe.cuh -- a whole mixture-of-experts layer for a few tokens in one
+// cooperative kernel.
+//
+//   l = x R^T, p = softmax(l), the top_k experts of each token by l (ties: the
+//   lowest index), h_e = silu(W1_e x) * (W3_e x), y = sum_e g_e W2_e h_e
+//
+// with W1, W3, W2 in 8 bits and one fp32 scale per 128 x 128 block.
+//
+// What bounds it: a few tokens read every weight of the experts they reach
+// once, so the floor is those bytes at HBM speed; everything else is kept out
+// of the stream's way.
+//
+// Activations at full precision on 8-bit tensor cores.  Weights go to the
+// tensor cores as they are stored (no decoding in the SMs), so the
+// activations have to be 8-bit too -- but not rounded to it: a value is the
+// sum of four e4m3 digits, v = s (d0 + d1/16 + d2/256 + d3/4096), s the power
+// of two that puts the largest value of a block of 128 in [128, 256).  Each
+// digit is the rounded remainder of the ones before it, 16 times larger, so
+// four digits carry 19 bits of a block's large values (fp16 has 11, bf16 8:
+// both exact) and an absolute error of 2^-29 of the block's largest for small
+// ones.  A token is then four columns of the product, weights take the 128
+// lanes (the MMA's M), and the digits' columns are joined in fp32 when the
+// block's sum is scaled.
+//
+// Work.  A persistent CTA per SM; three phases with two grid-wide barriers:
+//   0  router logits and the digits of x, spread over all warps of the grid;
+//   1  every CTA routes for itself (the logits are a few KB), then gate and
+//      up products: units (expert, 128 columns of the inner size, block of K)
+//      in one sequence cut evenly over the CTAs, so that no SM is left with a
+//      whole tile more than another.  Pieces of a tile meet in the workspace;
+//      the CTA that brings the last one adds them in CTA order (bitwise
+//      reproducible whoever is last), applies silu(gate) * up and writes the
+//      digits of h;
+//   2  down products: units (128 rows of y, expert, block of the inner size),
+//      cut the same way; a token's experts are added in registers and shared
+//      memory before anything leaves the SM, and the last piece of a row tile
+//      writes y.
+// The weights' ring runs through phases 1 and 2 without a stop: the first
+// tiles of phase 2 are on their way while the CTA waits for the last h.
+//
+// Warps: 0 weights (TMA), 1 TMEM and matrix instructions, 2 digits of x or h
+// (TMA, four rows a token) and scales, 3 idle after phase 1's routing,
+// 4-11 promotion (phase 1: 4-7 gate rows, 8-11 up rows; phase 2: both halves
+// hold the rows, alternate groups of four tokens).
+#pragma once
+
+#include "fp8_common.cuh"
+
+namespace sqz {
+namespace moe {
+
+using namespace f8;
+
+constexpr int kMaxTokens = 32;
+constexpr int kMaxExperts = 1024;
+constexpr int kMaxTopK = 16;
+constexpr int kMaxPairs = kMaxTokens * kMaxTopK;
+constexpr int kThreads = 384;
+constexpr int kWarps = kThreads / 32;
+constexpr int kMaxRing = 12;
+constexpr int kScaleSlots = 8;
+constexpr int kDigits = 4;
+
+// Start of the caller's workspace.  Zero before the first call; every call
+// leaves the tile counters zero and the barrier counter a multiple of the
+// grid.
+struct Header {
+    unsigned long long arrived;  // grid-wide barrier arrivals, ever
+    int status;
+    int pad;
+};
+
+struct Params {
+    const uint16_t* x;
+    int64_t ldx;
+    const uint16_t* router;
+    int64_t ld_router;
+    const float* s13;  // [experts][2][tiles_i][nkb_h]
+    const float* s2;   // [experts][tiles_h][nkb_i]
+    void* y;
+    int64_t ldy;
+    int32_t* ids;    // [tokens][top_k] or nullptr
+    float* weights;  // [tokens][top_k] or nullptr
+    // workspace
+    Header* head;
+    int* cnt1;       // [experts * tiles_i]
+    int* cnt2;       // [tiles_h]
+    float* logits;   // [tokens][experts]
+    uint8_t* xq;     // [tokens][4][hpad]
+    float* sx;       // [tokens][nkb_h]
+    uint8_t* hq;     // [pairs][4][ipad]
+    float* sh;       // [pairs][nkb_i]
+    float* part1;    // [grid][2][tokens][256]
+    float* part2;    // [grid][2][tokens][128]
+    int tokens, experts, top_k, hidden, inter;
+    int tiles_i, tiles_h;  // also the blocks of K of the down and the gate/up products
+    int hpad, ipad;
+    int bf16, renormalize, vec;
+    int stages, stage_bytes;
+};
+
+__host__ __device__ inline int b_rows(int tokens) { return (kDigits * tokens + 15) / 16 * 16; }
+
+__device__ __forceinline__ float load_x(const uint16_t* p, bool bf16) {
+    const uint16_t h = __ldg(p);
+    return bf16 ? __uint_as_float((uint32_t)h << 16) : __half2float(__ushort_as_half(h));
+}
+
+// ---------------------------------------------------------- grid barrier
+__device__ __forceinline__ unsigned long long ld_acquire(const unsigned long long* p) {
+    unsigned long long v;
+    asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(p) : "memory");
+    return v;
+}
+__device__ __forceinline__ void fence_proxy_all() { asm volatile("fence.proxy.async;" ::: "memory"); }
+
+// One thread of a CTA arrives, and later waits for the round its arrival
+// belongs to.  The grid is launched cooperatively (every CTA is resident), and
+// the wait is bounded all the same (about four seconds).
+__device__ __forceinline__ unsigned long long grid_arrive(Header* h) {
+    __threadfence();
+    const unsigned long long old = atomicAdd(&h->arrived, 1ull);
+    return (old / gridDim.x + 1) * gridDim.x;
+}
+__device__ __forceinline__ bool grid_wait(const Header* h, unsigned long long target, volatile int* dead) {
+    const long long t0 = clock64();
+    while (ld_acquire(&h->arrived) < target) {
+        if (*dead || clock64() - t0 > 8000000000ll) {
+            *dead = 1;
+            return false;
+        }
+    }
+    __threadfence();
+    return true;
+}
+
+// ------------------------------------------------------------ digits of v
+// Power of two that brings values up to `max_bits` (fp32 bits) into [128,
+// 256): the factor, and its inverse, which scales the sums back.  Exponents
+// below 2^-110 are treated as 2^-110 (both stay normal numbers).
+__device__ __forceinline__ float digit_scale(uint32_t max_bits, float* factor) {
+    int e = (int)(max_bits >> 23) - 127;
+    if (max_bits == 0 || max_bits >= 0x7F800000u) e = 7;  // zeros, or the digits are NaN
+    if (e < -110) e = -110;
+    *factor = __uint_as_float((uint32_t)(7 - e + 127) << 23);
+    return __uint_as_float((uint32_t)(e - 7 + 127) << 23);
+}
+// The four digits of v (already scaled), lowest byte first; NaN for a value
+// that is not finite.
+__device__ __forceinline__ uint32_t digits_of(float v) {
+    uint32_t out = 0;
+    if (!(fabsf(v) < __int_as_float(0x7F800000))) return 0x7F7F7F7Fu;
+#pragma unroll
+    for (int p = 0; p < kDigits; ++p) {
+        uint16_t code;
+        uint32_t back;
+        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(code) : "f"(0.f), "f"(v));
+        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(back) : "h"(code));
+        out |= (uint32_t)(code & 0xFF) << (8 * p);
+        v = (v - __half2float(__ushort_as_half((uint16_t)(back & 0xFFFF)))) * 16.f;
+    }
+    return out;
+}
+
+// ------------------------------------------------------------ phase 0
+// Logits of expert e for tokens t0 .. t0 + 3.
+__device__ __forceinline__ void logits_unit(const Params& p, int e, int t0, int lane) {
+    const uint16_t* r = p.router + (int64_t)e * p.ld_router;
+    const int n = min(4, p.tokens - t0);
+    float acc[4] = {0.f, 0.f, 0.f, 0.f};
+    if (p.vec) {
+#pragma unroll 4
+        for (int c = lane * 8; c < p.hidden; c += 256) {
+            const uint4 ru = ldg_u128(r + c);
+            const uint32_t rw[4] = {ru.x, ru.y, ru.z, ru.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (i < n) {
+                    const uint4 xu = ldg_u128(p.x + (int64_t)(t0 + i) * p.ldx + c);
+                    const uint32_t xw[4] = {xu.x, xu.y, xu.z, xu.w};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        float r0, r1, x0, x1;
+                        if (p.bf16) {
+                            r0 = __uint_as_float(rw[j] << 16), r1 = __uint_as_float(rw[j] & 0xFFFF0000u);
+                            x0 = __uint_as_float(xw[j] << 16), x1 = __uint_as_float(xw[j] & 0xFFFF0000u);
+                        } else {
+                            r0 = h2f((uint16_t)rw[j]), r1 = h2f((uint16_t)(rw[j] >> 16));
+                            x0 = h2f((uint16_t)xw[j]), x1 = h2f((uint16_t)(xw[j] >> 16));
+                        }
+                        acc[i] = fmaf(r0, x0, acc[i]);
+                        acc[i] = fmaf(r1, x1, acc[i]);
+                    }
+                }
+            }
+        }
+    } else {
+        for (int c = lane; c < p.hidden; c += 32) {
+            const float rv = load_x(r + c, p.bf16);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (i < n) acc[i] = fmaf(rv, load_x(p.x + (int64_t)(t0 + i) * p.ldx + c, p.bf16), acc[i]);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float v = warp_sum(acc[i]);
+        if (lane == 0 && i < n) p.logits[(t0 + i) * p.experts + e] = v;
+    }
+}
+
+// Digits of block kb of token t: lane holds four consecutive values.
+__device__ __forceinline__ void x_digits_unit(const Params& p, int t, int kb, int lane) {
+    float v[4];
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int c = kb * kBlockK + lane * 4 + j;
+        v[j] = c < p.hidden ? load_x(p.x + (int64_t)t * p.ldx + c, p.bf16) : 0.f;
+        m = max(m, __float_as_uint(v[j]) & 0x7FFFFFFFu);
+    }
+    m = __reduce_max_sync(0xffffffffu, m);
+    float f;
+    const float s = digit_scale(m, &f);
+    uint32_t d[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) d[j] = digits_of(v[j] * f);
+#pragma unroll
+    for (int q = 0; q < kDigits; ++q) {
+        uint32_t w = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w |= ((d[j] >> (8 * q)) & 0xFF) << (8 * j);
+        *reinterpret_cast<uint32_t*>(p.xq + ((int64_t)t * kDigits + q) * p.hpad + kb * kBlockK + lane * 4) = w;
+    }
+    if (lane == 0) p.sx[t * p.tiles_h + kb] = s;
+}
+
+// ------------------------------------------------------------ routing
+struct Routing {
+    uint32_t mask[kMaxExperts];     // tokens of each expert, one bit each
+    uint16_t base[kMaxExperts];     // first row of the expert's tokens
+    uint16_t active[kMaxPairs];     // experts with tokens, ascending
+    uint16_t id[kMaxPairs];         // [token][slot]
+    float weight[kMaxPairs];        // [token][slot]
+    uint8_t row_token[kMaxPairs];   // [row]: rows sorted by expert, then token
+    float row_weight[kMaxPairs];
+    int n_active;
+};
+
+// The choice of one token by one warp: top_k rounds of the warp's best
+// (highest logit, lowest index; NaN below everything).
+__device__ __forceinline__ void route_token(const Params& p, Routing* R, int t, int lane) {
+    const float* l = p.logits + t * p.experts;
+    float v[kMaxExperts / 32];
+    float top = -__int_as_float(0x7F800000);
+    bool nan = false;
+#pragma unroll
+    for (int i = 0; i < kMaxExperts / 32; ++i) {
+        const int e = i * 32 + lane;
+        if (i * 32 >= p.experts) break;
+        v[i] = e < p.experts ? __ldcg(l + e) : -__int_as_float(0x7F800000);
+        nan |= v[i] != v[i];
+        top = fmaxf(top, v[i]);
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+    nan = __any_sync(0xffffffffu, nan);
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < kMaxExperts / 32; ++i) {
+        if (i * 32 >= p.experts) break;
+        if (i * 32 + lane < p.experts) sum += expf(v[i] - top);
+    }
+    sum = warp_sum(sum);
+    uint32_t taken = 0;  // bit i: v[i] is out (taken, or past the experts)
+#pragma unroll
+    for (int i = 0; i < kMaxExperts / 32; ++i)
+        if (i * 32 + lane >= p.experts) taken |= 1u << i;
+    float mine = 0.f, chosen_sum = 0.f;
+    int mine_id = 0;
+    for (int j = 0; j < p.top_k; ++j) {
+        // the lane's best: highest value, lowest index; NaN below everything
+        float best = 0.f;
+        int at = -1;
+#pragma unroll
+        for (int i = 0; i < kMaxExperts / 32; ++i) {
+            if (i * 32 >= p.experts) break;
+            if (!(taken >> i & 1) && (at < 0 || v[i] > best || (best != best && v[i] == v[i]))) best = v[i], at = i;
+        }
+        // order as integers: value, then the lower index; 0 for a lane with nothing left
+        uint32_t key = 0;
+        if (at >= 0) {
+            const uint32_t u = __float_as_uint(best + 0.f);  // -0 and +0 are one value
+            key = best != best ? 1u : (u & 0x80000000u ? ~u : u | 0x80000000u);
+        }
+        const uint32_t high = __reduce_max_sync(0xffffffffu, key);
+        const uint32_t cand = key == high && at >= 0 ? (uint32_t)(at * 32 + lane) : 0xffffffffu;
+        const uint32_t e = __reduce_min_sync(0xffffffffu, cand);
+        if (cand == e) taken |= 1u << at;
+        const float lv = __shfl_sync(0xffffffffu, best, e & 31);
+        const float w = expf(lv - top) / sum;
+        chosen_sum += w;
+        if (lane == j) mine = w, mine_id = (int)e;
+    }
+    if (lane < p.top_k) {
+        float w = p.renormalize ? mine / chosen_sum : mine;
+        if (nan) w = __int_as_float(0x7FFFFFFF);
+        R->id[t * p.top_k + lane] = (uint16_t)mine_id;
+        R->weight[t * p.top_k + lane] = w;
+        atomicOr(&R->mask[mine_id], 1u << t);
+        if (blockIdx.x == 0) {
+            if (p.ids) p.ids[t * p.top_k + lane] = mine_id;
+            if (p.weights) p.weights[t * p.top_k + lane] = w;
+        }
+    }
+}
+
+// Active experts in ascending order and the first row of each (one warp).
+__device__ __forceinline__ void list_experts(const Params& p, Routing* R, int lane) {
+    int n = 0, rows = 0;
+    for (int e0 = 0; e0 < p.experts; e0 += 32) {
+        const int e = e0 + lane;
+        const int c = e < p.experts ? __popc(R->mask[e]) : 0;
+        const uint32_t on = __ballot_sync(0xffffffffu, c > 0);
+        if (on == 0) continue;
+        int pre = c;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int o = __shfl_up_sync(0xffffffffu, pre, off);
+            if (lane >= off) pre += o;
+        }
+        if (c > 0) {
+            R->active[n + __popc(on & ((1u << lane) - 1))] = (uint16_t)e;
+            R->base[e] = (uint16_t)(rows + pre - c);
+        }
+        n += __popc(on);
+        rows += __shfl_sync(0xffffffffu, pre, 31);
+    }
+    if (lane == 0) R->n_active = n;
+}
+
+// -------------------------------------------------------- unit sequences
+// `total` units cut evenly: CTA c has [begin(c), begin(c + 1)).
+__device__ __forceinline__ int cut(int total, int c) { return (int)((int64_t)total * c / gridDim.x); }
+// The CTA that has unit u.
+__device__ __forceinline__ int owner(int total, int u) {
+    return (int)((((int64_t)u + 1) * gridDim.x - 1) / total);
+}
+
+struct Shared {
+    Routing route;
+    uint64_t full[kMaxRing], empty[kMaxRing], sfull[kScaleSlots], sempty[kScaleSlots], tfull[2], tempty[2];
+    float scale[kScaleSlots][kMaxTokens + 2];  // token (or row) scales, the two weight scales
+    uint32_t taddr;
+    uint64_t h_arrived;              // the CTA's last h is written and its arrival posted
+    unsigned long long h_target;     // the barrier round of that arrival
+    int dead, last;
+    uint32_t max_bits[4][kMaxTokens];
+};
+
+__device__ __forceinline__ void bar_promotion() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+
+// acc[i] += scale_i * sw * (four digits' columns) for the tokens of group b
+// (four tokens = 16 columns).
+__device__ __forceinline__ void promote4(float (&acc)[4], uint32_t taddr, const float* sc, float sw) {
+    uint32_t d[16];
+    tmem_ld16(taddr, d);
+    tmem_wait_ld(d);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float v = __uint_as_float(d[4 * i + 3]);
+        v = fmaf(v, 0.0625f, __uint_as_float(d[4 * i + 2]));
+        v = fmaf(v, 0.0625f, __uint_as_float(d[4 * i + 1]));
+        v = fmaf(v, 0.0625f, __uint_as_float(d[4 * i]));
+        acc[i] = fmaf(v, sc[i] * sw, acc[i]);
+    }
+}
+
+__global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant__ CUtensorMap map_w13,
+                                                          const __grid_constant__ CUtensorMap map_w2,
+                                                          const __grid_constant__ CUtensorMap map_x,
+                                                          const __grid_constant__ CUtensorMap map_h, const Params p) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* ring = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+    float* sums = reinterpret_cast<float*>(ring + p.stages * p.stage_bytes);  // [2][tokens][128]
+    Shared* S = reinterpret_cast<Shared*>(sums + 2 * p.tokens * 128);
+    Routing* R = &S->route;
+    volatile int* dead = &S->dead;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int nkb1 = p.tiles_h, nkb2 = p.tiles_i;  // blocks of K of the two products
+
+    if (warp == 1) tmem_alloc(&S->taddr, 512);
+    if (threadIdx.x == 0) {
+        S->dead = 0;
+        for (int i = 0; i < p.stages; ++i) {
+            mbar_init(&S->full[i], 1 + 1);
+            mbar_init(&S->empty[i], 1);
+        }
+        for (int i = 0; i < kScaleSlots; ++i) {
+            mbar_init(&S->sfull[i], 32);
+            mbar_init(&S->sempty[i], 8);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&S->tfull[i], 1);
+            mbar_init(&S->tempty[i], 8);
+        }
+        mbar_init(&S->h_arrived, 1);
+        fence_mbar_init();
+    }
+    for (int e = threadIdx.x; e < p.experts; e += kThreads) R->mask[e] = 0;
+    // ---- phase 0: logits and the digits of x
+    {
+        const int groups = (p.tokens + 3) / 4, n_logits = p.experts * groups, n_all = n_logits + p.tokens * nkb1;
+        for (int u = blockIdx.x + gridDim.x * warp; u < n_all; u += gridDim.x * kWarps) {
+            if (u < n_logits)
+                logits_unit(p, u / groups, u % groups * 4, lane);
+            else
+                x_digits_unit(p, (u - n_logits) / nkb1, (u - n_logits) % nkb1, lane);
+        }
+    }
+    fence_proxy_all();  // the digits are read by TMA
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t taddr = S->taddr;
+    if (threadIdx.x == 0) grid_wait(p.head, grid_arrive(p.head), dead);
+    __syncthreads();
+    fence_proxy_all();
+
+    // ---- routing, by every CTA for itself
+    if (!*dead) {
+        for (int t = warp; t < p.tokens; t += kWarps) route_token(p, R, t, lane);
+    }
+    __syncthreads();
+    if (warp == 0) list_experts(p, R, lane);
+    __syncthreads();
+    for (int i = threadIdx.x; i < p.tokens * p.top_k; i += kThreads) {
+        const int t = i / p.top_k, e = R->id[i];
+        const int row = R->base[e] + __popc(R->mask[e] & ((1u << t) - 1));
+        R->row_token[row] = (uint8_t)t;
+        R->row_weight[row] = R->weight[i];
+    }
+    __syncthreads();
+
+    const int n_act = *dead ? 0 : R->n_active;
+    const int total1 = n_act * p.tiles_i * nkb1, total2 = p.tiles_h * n_act * nkb2;
+    const int u1a = cut(total1, blockIdx.x), u1b = cut(total1, blockIdx.x + 1);
+    const int u2a = cut(total2, blockIdx.x), u2b = cut(total2, blockIdx.x + 1);
+
+    if (warp == 0) {  // ---------------------------------------------- weights
+        if (lane == 0) {
+            int st = 0, ph = 0;
+            bool alive = true;
+            for (int u = u1a; u < u1b && alive; ++u) {
+                const int tile = u / nkb1, kb = u - tile * nkb1, a = tile / p.tiles_i, ti = tile - a * p.tiles_i;
+                const int e = R->active[a];
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    if (!(alive = wait_alive(&S->empty[st], ph ^ 1, dead))) break;
+                    mbar_expect_tx(&S->full[st], kTileBytes);
+                    tma_load_3d(ring + st * p.stage_bytes, &map_w13, &S->full[st], kb * kBlockK, ti * 128, 2 * e + half);
+                    if (++st == p.stages) st = 0, ph ^= 1;
+                }
+            }
+            for (int u = u2a; u < u2b && alive; ++u) {
+                const int run = u / nkb2, kb = u - run * nkb2, rt = run / n_act, a = run - rt * n_act;
+                if (!(alive = wait_alive(&S->empty[st], ph ^ 1, dead))) break;
+                mbar_expect_tx(&S->full[st], kTileBytes);
+                tma_load_3d(ring + st * p.stage_bytes, &map_w2, &S->full[st], kb * kBlockK, rt * 128, R->active[a]);
+                if (++st == p.stages) st = 0, ph ^= 1;
+            }
+            if (!alive) let_copies_land();
+        }
+    } else if (warp == 1) {  // ---------------------------- matrix instructions
+        if (lane == 0) {
+            int st = 0, ph = 0;
+            uint32_t it = 0;
+            bool alive = true;
+            for (int u = u1a; u < u1b && alive; ++u, ++it) {
+                const int a = u / nkb1 / p.tiles_i, n = __popc(R->mask[R->active[a]]);
+                const uint32_t idesc = instr_desc(0, 0, 128, b_rows(n));
+                const int buf = it & 1;
+                alive = wait_alive(&S->tempty[buf], ((it >> 1) & 1) ^ 1, dead);
+                uint32_t b = 0, first = 0;
+#pragma unroll
+                for (int half = 0; half < 2 && alive; ++half) {
+                    if (!(alive = wait_alive(&S->full[st], ph, dead))) break;
+                    tc_fence_after();
+                    const uint32_t at = smem_u32(ring + st * p.stage_bytes);
+                    if (half == 0) b = at + kTileBytes, first = st;  // the up tile shares the gate tile's digits
+                    mma_block(taddr + buf * 256 + half * 128, at, b, idesc);
+                    if (half == 1) {
+                        mma_commit(&S->empty[first]);
+                        mma_commit(&S->empty[st]);
+                        mma_commit(&S->tfull[buf]);
+                    }
+                    if (++st == p.stages) st = 0, ph ^= 1;
+                }
+            }
+            for (int u = u2a; u < u2b && alive; ++u, ++it) {
+                const int run = u / nkb2, a = run % n_act, n = __popc(R->mask[R->active[a]]);
+                const uint32_t idesc = instr_desc(0, 0, 128, b_rows(n));
+                const int buf = it & 1;
+                alive = wait_alive(&S->tempty[buf], ((it >> 1) & 1) ^ 1, dead) && wait_alive(&S->full[st], ph, dead);
+                if (!alive) break;
+                tc_fence_after();
+                const uint32_t at = smem_u32(ring + st * p.stage_bytes);
+                mma_block(taddr + buf * 256, at, at + kTileBytes, idesc);
+                mma_commit(&S->empty[st]);
+                mma_commit(&S->tfull[buf]);
+                if (++st == p.stages) st = 0, ph ^= 1;
+            }
+            if (!alive) let_copies_land();
+        }
+    } else if (warp == 2) {  // ------------------------ digits and their scales
+        int st = 0, ph = 0;
+        uint32_t it = 0;
+        bool alive = true;
+        for (int u = u1a; u < u1b && alive; ++u, ++it) {
+            const int tile = u / nkb1, kb = u - tile * nkb1, a = tile / p.tiles_i, ti = tile - a * p.tiles_i;
+            const int e = R->active[a], n = __popc(R->mask[e]);
+            const int t = lane < n ? R->row_token[R->base[e] + lane] : 0, slot = it % kScaleSlots;
+            alive = __all_sync(0xffffffffu, wait_alive(&S->sempty[slot], ((it / kScaleSlots) & 1) ^ 1, dead) &&
+                                                wait_alive(&S->empty[st], ph ^ 1, dead));
+            if (!alive) break;
+            if (lane < n) cp_async4(&S->scale[slot][lane], p.sx + t * nkb1 + kb, true);
+            if (lane < 2)
+                cp_async4(&S->scale[slot][kMaxTokens + lane],
+                          p.s13 + (((int64_t)e * 2 + lane) * p.tiles_i + ti) * nkb1 + kb, true);
+            cp_async_arrive(&S->sfull[slot]);
+            if (lane == 0) mbar_expect_tx(&S->full[st], (uint32_t)n * kDigits * kBlockK);
+            __syncwarp();
+            if (lane < n)
+                tma_load_2d(ring + st * p.stage_bytes + kTileBytes + lane * kDigits * kBlockK, &map_x, &S->full[st],
+                            kb * kBlockK, t * kDigits);
+            if (++st == p.stages) st = 0, ph ^= 1;
+            // the up tile's stage brings no digits of its own
+            alive = __all_sync(0xffffffffu, wait_alive(&S->empty[st], ph ^ 1, dead));
+            if (!alive) break;
+            if (lane == 0) mbar_arrive(&S->full[st]);
+            if (++st == p.stages) st = 0, ph ^= 1;
+        }
+        // every h of the grid has to be there
+        if (u2a < u2b && alive) {
+            bool ok = true;
+            if (lane == 0) ok = wait_alive(&S->h_arrived, 0, dead) && grid_wait(p.head, S->h_target, dead);
+            alive = __all_sync(0xffffffffu, ok);
+            fence_proxy_all();
+        }
+        for (int u = u2a; u < u2b && alive; ++u, ++it) {
+            const int run = u / nkb2, kb = u - run * nkb2, rt = run / n_act, a = run - rt * n_act;
+            const int e = R->active[a], n = __popc(R->mask[e]), row0 = R->base[e], slot = it % kScaleSlots;
+            alive = __all_sync(0xffffffffu, wait_alive(&S->sempty[slot], ((it / kScaleSlots) & 1) ^ 1, dead) &&
+                                                wait_alive(&S->empty[st], ph ^ 1, dead));
+            if (!alive) break;
+            if (lane < n) cp_async4(&S->scale[slot][lane], p.sh + (int64_t)(row0 + lane) * nkb2 + kb, true);
+            if (lane == 0)
+                cp_async4(&S->scale[slot][kMaxTokens], p.s2 + ((int64_t)e * p.tiles_h + rt) * nkb2 + kb, true);
+            cp_async_arrive(&S->sfull[slot]);
+            if (lane == 0) mbar_expect_tx(&S->full[st], (uint32_t)n * kDigits * kBlockK);
+            __syncwarp();
+            if (lane < n)
+                tma_load_2d(ring + st * p.stage_bytes + kTileBytes + lane * kDigits * kBlockK, &map_h, &S->full[st],
+                            kb * kBlockK, (row0 + lane) * kDigits);
+            if (++st == p.stages) st = 0, ph ^= 1;
+        }
+    } else if (warp >= 4) {  // ------------------------------------- promotion
+        const int group = (warp - 4) / 4, r = (warp & 3) * 32 + lane;
+        const bool first_thread = warp == 4 && lane == 0;
+        const uint32_t lanes = taddr + ((uint32_t)(warp & 3) << 21);
+        uint32_t it = 0;
+        // Once a wait has given up, the warps stop waiting but keep step (they
+        // meet at barriers); the results are then undefined.
+        bool alive = true;
+        // Waits for unit `it`: its scales and its sums.  Returns the scales.
+        const auto unit_ready = [&]() -> const float* {
+            const int slot = it % kScaleSlots;
+            if (alive)
+                alive = __all_sync(0xffffffffu, wait_alive(&S->sfull[slot], (it / kScaleSlots) & 1, dead) &&
+                                                    wait_alive(&S->tfull[it & 1], (it >> 1) & 1, dead));
+            tc_fence_after();
+            return S->scale[slot];
+        };
+        const auto unit_done = [&]() {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&S->tempty[it & 1]);
+                mbar_arrive(&S->sempty[it % kScaleSlots]);
+            }
+            ++it;
+        };
+        // Adds `len` of a tile's `whole` units to its counter once the pieces
+        // of all 256 threads are written; true for the CTA that completes it.
+        const auto is_last = [&](int* counter, int len, int whole) {
+            __threadfence();
+            bar_promotion();
+            if (first_thread) {
+                const int old = atomicAdd(counter, len);
+                S->last = old + len == whole;
+                if (S->last) *counter = 0;  // for the next call
+            }
+            bar_promotion();
+            if (S->last) __threadfence();
+            return S->last != 0;
+        };
+
+        for (int u = u1a; u < u1b;) {
+            const int tile = u / nkb1, k0 = u - tile * nkb1, len = min(nkb1 - k0, u1b - u);
+            const int a = tile / p.tiles_i, ti = tile - a * p.tiles_i, e = R->active[a];
+            const int n = __popc(R->mask[e]), row0 = R->base[e];
+            float acc[8][4];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) acc[i / 4][i % 4] = 0.f;
+            for (int i = 0; i < len; ++i) {
+                const float* sc = unit_ready();
+                const float sw = sc[kMaxTokens + group];
+#pragma unroll
+                for (int b = 0; b < 8; ++b)
+                    if (4 * b < n) promote4(acc[b], lanes + (it & 1) * 256 + group * 128 + b * 16, sc + 4 * b, sw);
+                unit_done();
+            }
+            bool mine = len == nkb1;
+            if (!mine) {  // a piece: at the tile's start (then the CTA's last tile) or not (then its first)
+                float* dst = p.part1 + ((int64_t)(blockIdx.x * 2 + (k0 > 0 ? 0 : 1)) * p.tokens) * 256 + group * 128 + r;
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    if (i < n) __stcg(dst + i * 256, acc[i / 4][i % 4]);
+                if ((mine = is_last(p.cnt1 + tile, len, nkb1))) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) acc[i / 4][i % 4] = 0.f;
+                    const int t0 = tile * nkb1, c1 = owner(total1, t0 + nkb1 - 1);
+                    for (int c = owner(total1, t0); c <= c1; ++c) {
+                        const int ca = cut(total1, c);
+                        if (ca == cut(total1, c + 1)) continue;
+                        const float* src =
+                            p.part1 + ((int64_t)(c * 2 + (ca > t0 ? 0 : 1)) * p.tokens) * 256 + group * 128 + r;
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (i < n) acc[i / 4][i % 4] += __ldcg(src + i * 256);
+                    }
+                }
+            }
+            if (mine) {  // h = silu(gate) * up, and its digits
+                if (group == 1) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        if (i < n) sums[i * 128 + r] = acc[i / 4][i % 4];
+                }
+                bar_promotion();
+                if (group == 0) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        if (i < n) {
+                            const float g = acc[i / 4][i % 4], h = g / (1.f + expf(-g)) * sums[i * 128 + r];
+                            acc[i / 4][i % 4] = h;
+                            const uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(h) & 0x7FFFFFFFu);
+                            if (lane == 0) S->max_bits[warp & 3][i] = m;
+                        }
+                    }
+                    asm volatile("bar.sync 2, 128;" ::: "memory");
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        if (i < n) {
+                            float f;
+                            const float s = digit_scale(max(max(S->max_bits[0][i], S->max_bits[1][i]),
+                                                            max(S->max_bits[2][i], S->max_bits[3][i])),
+                                                        &f);
+                            const uint32_t d = digits_of(acc[i / 4][i % 4] * f);
+                            uint8_t* dst = p.hq + (int64_t)(row0 + i) * kDigits * p.ipad + ti * 128 + r;
+#pragma unroll
+                            for (int q = 0; q < kDigits; ++q) dst[(int64_t)q * p.ipad] = (uint8_t)(d >> (8 * q));
+                            if (r == 0) p.sh[(int64_t)(row0 + i) * nkb2 + ti] = s;
+                        }
+                    }
+                }
+                bar_promotion();  // `sums` is read
+            }
+            u += len;
+        }
+        __threadfence();
+        fence_proxy_all();  // the digits are read by TMA
+        bar_promotion();
+        if (first_thread) {
+            S->h_target = grid_arrive(p.head);
+            mbar_arrive(&S->h_arrived);
+        }
+
+        for (int u = u2a; u < u2b;) {
+            const int per = n_act * nkb2, rt = u / per, k0 = u - rt * per, len = min(per - k0, u2b - u);
+            float* own = sums + group * p.tokens * 128 + r;  // [token][128], this thread's row
+            for (int t = 0; t < p.tokens; ++t) own[t * 128] = 0.f;
+            for (int v = k0; v < k0 + len;) {
+                const int a = v / nkb2, kb = v - a * nkb2, run = min(nkb2 - kb, k0 + len - v);
+                const int e = R->active[a], n = __popc(R->mask[e]), row0 = R->base[e];
+                float acc[4][4];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) acc[i / 4][i % 4] = 0.f;
+                for (int i = 0; i < run; ++i) {
+                    const float* sc = unit_ready();
+                    const float sw = sc[kMaxTokens];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int b = 2 * j + group;
+                        if (4 * b < n) promote4(acc[j], lanes + (it & 1) * 256 + b * 16, sc + 4 * b, sw);
+                    }
+                    unit_done();
+                }
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const int row = (2 * (i / 4) + group) * 4 + i % 4;
+                    if (row < n)
+                        own[R->row_token[row0 + row] * 128] =
+                            fmaf(R->row_weight[row0 + row], acc[i / 4][i % 4], own[R->row_token[row0 + row] * 128]);
+                }
+                v += run;
+            }
+            bar_promotion();
+            // the two groups' sums; group g finishes the tokens of its parity
+            bool mine = len == per;
+            const float* other = sums + r;
+            if (!mine) {
+                float* dst = p.part2 + ((int64_t)(blockIdx.x * 2 + (k0 > 0 ? 0 : 1)) * p.tokens) * 128 + r;
+                for (int t = group; t < p.tokens; t += 2)
+                    __stcg(dst + t * 128, other[t * 128] + other[(p.tokens + t) * 128]);
+                mine = is_last(p.cnt2 + rt, len, per);
+            }
+            if (mine && rt * 128 + r < p.hidden) {
+                const int t0 = rt * per, c0 = owner(total2, t0), c1 = owner(total2, t0 + per - 1);
+                for (int t = group; t < p.tokens; t += 2) {
+                    float v = 0.f;
+                    if (len == per) {
+                        v = other[t * 128] + other[(p.tokens + t) * 128];
+                    } else {
+                        for (int c = c0; c <= c1; ++c) {
+                            const int ca = cut(total2, c);
+                            if (ca == cut(total2, c + 1)) continue;
+                            v += __ldcg(p.part2 + ((int64_t)(c * 2 + (ca > t0 ? 0 : 1)) * p.tokens + t) * 128 + r);
+                        }
+                    }
+                    store_out(p.y, t * p.ldy + rt * 128 + r, p.bf16 ? kBF16 : kF16, v);
+                }
+            }
+            bar_promotion();  // `sums` is read
+            u += len;
+        }
+    }
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc(taddr, 512);
+    if (threadIdx.x == 0 && *dead) atomicOr(&p.head->status, 1);
+}
+
+}  // namespace moe
+}  // namespace sqz
