@@ -25,7 +25,6 @@ using tc::fence_mbar_init;
 using tc::mbar_arrive;
 using tc::mbar_expect_tx;
 using tc::mbar_init;
-using tc::mbar_try_wait;
 using tc::pdl_launch_dependents;
 using tc::pdl_wait_previous;
 using tc::smem_u32;
@@ -35,16 +34,34 @@ constexpr int kTileBytes = 128 * 128; // a tile of 128 rows
 
 enum OutType : int { kF16 = 0, kBF16 = 1, kF32 = 2 };
 
-// Waits are bounded (tc::kWaitLimit polls of tc::kSuspendNs, about two
-// seconds).  A wait that gives up sets `*dead` (shared memory), which ends
-// the other waits of the CTA too; the kernel then leaves in order.
-__device__ __forceinline__ bool wait_alive(uint64_t* bar, uint32_t parity, volatile int* dead) {
-    for (uint32_t i = 0; i < tc::kWaitLimit; ++i) {
-        if (mbar_try_wait(bar, parity)) return true;
+// Waits are bounded (kWaitCycles, about two seconds).  A wait that gives up
+// sets `*dead` (shared memory), which ends the other waits of the CTA too; the
+// kernel then leaves in order.  The polls carry no suspend-time hint: these
+// barriers complete every few hundred cycles, and a hinted wait wakes later.
+constexpr long long kWaitCycles = 4000000000ll;
+
+__device__ __forceinline__ bool mbar_poll(uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+__device__ __forceinline__ bool wait_long(uint64_t* bar, uint32_t parity, volatile int* dead) {
+    const long long t0 = clock64();
+    while (!mbar_poll(bar, parity)) {
         if (*dead) return false;
+        if (clock64() - t0 > kWaitCycles) {
+            *dead = 1;
+            return false;
+        }
     }
-    *dead = 1;
-    return false;
+    return true;
+}
+__device__ __forceinline__ bool wait_alive(uint64_t* bar, uint32_t parity, volatile int* dead) {
+    return mbar_poll(bar, parity) || wait_long(bar, parity, dead);
 }
 
 // After a wait gave up: time (100 ms) for the thread's own copies and matrix

@@ -213,14 +213,19 @@ constexpr int kMaxStages = 12;
 // bits every run.
 //
 //   warp 0: TMA loads of W and A tiles into a ring of stages
-//   warp 1: TMEM allocation, matrix instructions into one of two accumulators
+//   warp 1: TMEM allocation, matrix instructions into a ring of accumulators
 //   warp 2: the block's scales into the stage (4-byte asynchronous copies)
 //   warps 3-6: promotion; thread = a row of W
 template <int TB>
 struct FewShape {
     static constexpr int kStageBytes = kTileBytes + TB * kBlockK;
     static constexpr int kScaleFloats = TB + 4;  // TB token scales, the weights' scale
-    static constexpr int kTmemCols = 2 * TB < 32 ? 32 : 2 * TB;
+    // A block's way from the matrix instruction through the promotion and back
+    // to a free accumulator takes over a thousand cycles (barriers, mostly): two
+    // accumulators let a CTA do a block every 820, eight one every
+    // (half the tensor memory, so that two CTAs share an SM).
+    static constexpr int kBufs = 256 / TB < 8 ? 256 / TB : 8;
+    static constexpr int kTmemCols = kBufs * TB;
     static constexpr int kThreads = 224;
     static int smem_bytes(int stages) { return 1024 + stages * (kStageBytes + kScaleFloats * 4); }
 };
@@ -231,7 +236,7 @@ __global__ void __launch_bounds__(224) fp8_gemm_few_kernel(const __grid_constant
                                                             const GemmParams p) {
     using S = FewShape<TB>;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ uint64_t full[kMaxStages], empty[kMaxStages], tfull[2], tempty[2];
+    __shared__ uint64_t full[kMaxStages], empty[kMaxStages], tfull[S::kBufs], tempty[S::kBufs];
     __shared__ uint32_t taddr_s;
     __shared__ int dead_s;
     uint8_t* ring = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
@@ -251,7 +256,7 @@ __global__ void __launch_bounds__(224) fp8_gemm_few_kernel(const __grid_constant
             mbar_init(&full[i], 1 + 32);
             mbar_init(&empty[i], 1 + 4);
         }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < S::kBufs; ++i) {
             mbar_init(&tfull[i], 1);
             mbar_init(&tempty[i], 4);
         }
@@ -284,8 +289,8 @@ __global__ void __launch_bounds__(224) fp8_gemm_few_kernel(const __grid_constant
         if (lane == 0) {
             int st = 0, ph = 0;
             for (int it = 0; it < nk; ++it) {
-                const int buf = it & 1;
-                if (!wait_alive(&tempty[buf], ((it >> 1) & 1) ^ 1, dead) || !wait_alive(&full[st], ph, dead)) {
+                const int buf = it % S::kBufs;
+                if (!wait_alive(&tempty[buf], ((it / S::kBufs) & 1) ^ 1, dead) || !wait_alive(&full[st], ph, dead)) {
                     let_copies_land();
                     break;
                 }
@@ -319,9 +324,9 @@ __global__ void __launch_bounds__(224) fp8_gemm_few_kernel(const __grid_constant
         const uint32_t lanes = taddr + ((uint32_t)(warp & 3) << 21);
         int st = 0, ph = 0;
         for (int it = 0; it < nk; ++it) {
-            const int buf = it & 1;
+            const int buf = it % S::kBufs;
             bool ok = wait_alive(&full[st], ph, dead);  // the scales of the stage
-            ok = ok && wait_alive(&tfull[buf], (it >> 1) & 1, dead);
+            ok = ok && wait_alive(&tfull[buf], (it / S::kBufs) & 1, dead);
             if (!__all_sync(0xffffffffu, ok)) break;
             tc_fence_after();
             const float* sc = scales + st * S::kScaleFloats;

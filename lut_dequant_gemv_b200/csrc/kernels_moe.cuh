@@ -59,6 +59,7 @@ constexpr int kThreads = 384;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxRing = 12;
 constexpr int kScaleSlots = 8;
+constexpr int kMaxBufs = 8;  // accumulators in tensor memory (a power of two; see kernels_fp8.cuh)
 constexpr int kDigits = 4;
 
 // Start of the caller's workspace.  Zero before the first call; every call
@@ -163,50 +164,64 @@ __device__ __forceinline__ uint32_t digits_of(float v) {
 }
 
 // ------------------------------------------------------------ phase 0
-// Logits of expert e for tokens t0 .. t0 + 3.
-__device__ __forceinline__ void logits_unit(const Params& p, int e, int t0, int lane) {
-    const uint16_t* r = p.router + (int64_t)e * p.ld_router;
-    const int n = min(4, p.tokens - t0);
-    float acc[4] = {0.f, 0.f, 0.f, 0.f};
+__device__ __forceinline__ void unpack8(const uint4& u, bool bf16, float (&v)[8]) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        v[2 * j] = bf16 ? __uint_as_float(w[j] << 16) : h2f((uint16_t)w[j]);
+        v[2 * j + 1] = bf16 ? __uint_as_float(w[j] & 0xFFFF0000u) : h2f((uint16_t)(w[j] >> 16));
+    }
+}
+// Eight values from column c (zeros past `hidden`; a vector load when rows are
+// 16-byte aligned).
+__device__ __forceinline__ void load_x8(const uint16_t* row, int c, const Params& p, float (&v)[8]) {
     if (p.vec) {
-#pragma unroll 4
-        for (int c = lane * 8; c < p.hidden; c += 256) {
-            const uint4 ru = ldg_u128(r + c);
-            const uint32_t rw[4] = {ru.x, ru.y, ru.z, ru.w};
+        unpack8(c < p.hidden ? ldg_u128(row + c) : make_uint4(0, 0, 0, 0), p.bf16, v);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = c + j < p.hidden ? load_x(row + c + j, p.bf16) : 0.f;
+    }
+}
+
+// The logits of expert e for every token: the warp's share of the columns
+// (runs of 256, 8 a lane), then the lanes' sums; lane t returns token t's.
+// The expert's row is held in registers (two runs at a time), so a token costs
+// its own loads only; four tokens' sums cross the lanes together.
+__device__ __forceinline__ float logits_share(const Params& p, int e, int warp, int lane) {
+    const uint16_t* r = p.router + (int64_t)e * p.ld_router;
+    float mine = 0.f;
+    for (int c0 = warp * 256; c0 < p.hidden; c0 += 2 * kWarps * 256) {
+        const int ca = c0 + lane * 8, cb = ca + kWarps * 256;
+        float ra[8], rb[8];
+        load_x8(r, ca, p, ra);
+        load_x8(r, cb, p, rb);
+#pragma unroll 1
+        for (int t0 = 0; t0 < p.tokens; t0 += 4) {
+            float s[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                if (i < n) {
-                    const uint4 xu = ldg_u128(p.x + (int64_t)(t0 + i) * p.ldx + c);
-                    const uint32_t xw[4] = {xu.x, xu.y, xu.z, xu.w};
+                const uint16_t* x = p.x + (int64_t)min(t0 + i, p.tokens - 1) * p.ldx;
+                float xa[8], xb[8];
+                load_x8(x, ca, p, xa);
+                load_x8(x, cb, p, xb);
+                s[i] = 0.f;
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        float r0, r1, x0, x1;
-                        if (p.bf16) {
-                            r0 = __uint_as_float(rw[j] << 16), r1 = __uint_as_float(rw[j] & 0xFFFF0000u);
-                            x0 = __uint_as_float(xw[j] << 16), x1 = __uint_as_float(xw[j] & 0xFFFF0000u);
-                        } else {
-                            r0 = h2f((uint16_t)rw[j]), r1 = h2f((uint16_t)(rw[j] >> 16));
-                            x0 = h2f((uint16_t)xw[j]), x1 = h2f((uint16_t)(xw[j] >> 16));
-                        }
-                        acc[i] = fmaf(r0, x0, acc[i]);
-                        acc[i] = fmaf(r1, x1, acc[i]);
-                    }
-                }
+                for (int j = 0; j < 8; ++j) s[i] = fmaf(ra[j], xa[j], fmaf(rb[j], xb[j], s[i]));
             }
-        }
-    } else {
-        for (int c = lane; c < p.hidden; c += 32) {
-            const float rv = load_x(r + c, p.bf16);
+            // lanes 8 i .. 8 i + 7 end with token t0 + i
+            const bool up2 = lane & 16, up1 = lane & 8;
+            float k0 = up2 ? s[2] : s[0], k1 = up2 ? s[3] : s[1];
+            k0 += __shfl_xor_sync(0xffffffffu, up2 ? s[0] : s[2], 16);
+            k1 += __shfl_xor_sync(0xffffffffu, up2 ? s[1] : s[3], 16);
+            float v = up1 ? k1 : k0;
+            v += __shfl_xor_sync(0xffffffffu, up1 ? k0 : k1, 8);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (i < n) acc[i] = fmaf(rv, load_x(p.x + (int64_t)(t0 + i) * p.ldx + c, p.bf16), acc[i]);
+            for (int off = 4; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+            v = __shfl_sync(0xffffffffu, v, (lane - t0) * 8 & 31);
+            if (lane >= t0 && lane < t0 + 4) mine += v;
         }
     }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float v = warp_sum(acc[i]);
-        if (lane == 0 && i < n) p.logits[(t0 + i) * p.experts + e] = v;
-    }
+    return mine;
 }
 
 // Digits of block kb of token t: lane holds four consecutive values.
@@ -244,67 +259,54 @@ struct Routing {
     float weight[kMaxPairs];        // [token][slot]
     uint8_t row_token[kMaxPairs];   // [row]: rows sorted by expert, then token
     float row_weight[kMaxPairs];
-    int n_active;
+    int n_active, n_most;  // experts with tokens; the most tokens one has
 };
 
+// Logits as unsigned integers of the same order, +0 and -0 alike, NaN (1)
+// below every number; 0 is left for what is taken.
+__device__ __forceinline__ uint32_t logit_key(float l) {
+    const uint32_t u = __float_as_uint(l + 0.f);
+    return l != l ? 1u : (u & 0x80000000u ? ~u : u | 0x80000000u);
+}
+__device__ __forceinline__ float key_logit(uint32_t k) {
+    return k == 1u ? __int_as_float(0x7FFFFFFF) : __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
+}
+
 // The choice of one token by one warp: top_k rounds of the warp's best
-// (highest logit, lowest index; NaN below everything).
-__device__ __forceinline__ void route_token(const Params& p, Routing* R, int t, int lane) {
+// (highest logit, lowest index).  `keys`: the warp's copy, [experts].
+__device__ __forceinline__ void route_token(const Params& p, Routing* R, uint32_t* keys, int t, int lane) {
     const float* l = p.logits + t * p.experts;
-    float v[kMaxExperts / 32];
-    float top = -__int_as_float(0x7F800000);
-    bool nan = false;
-#pragma unroll
-    for (int i = 0; i < kMaxExperts / 32; ++i) {
-        const int e = i * 32 + lane;
-        if (i * 32 >= p.experts) break;
-        v[i] = e < p.experts ? __ldcg(l + e) : -__int_as_float(0x7F800000);
-        nan |= v[i] != v[i];
-        top = fmaxf(top, v[i]);
+    uint32_t best = 0;
+#pragma unroll 4
+    for (int e = lane; e < p.experts; e += 32) {
+        const uint32_t k = logit_key(__ldcg(l + e));
+        keys[e] = k;
+        best = max(best, k);
     }
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-    nan = __any_sync(0xffffffffu, nan);
-    float sum = 0.f;
-#pragma unroll
-    for (int i = 0; i < kMaxExperts / 32; ++i) {
-        if (i * 32 >= p.experts) break;
-        if (i * 32 + lane < p.experts) sum += expf(v[i] - top);
-    }
+    const float top = key_logit(__reduce_max_sync(0xffffffffu, best));
+    float sum = 0.f;  // NaN if any logit is (key_logit)
+#pragma unroll 2
+    for (int e = lane; e < p.experts; e += 32) sum += expf(key_logit(keys[e]) - top);
     sum = warp_sum(sum);
-    uint32_t taken = 0;  // bit i: v[i] is out (taken, or past the experts)
-#pragma unroll
-    for (int i = 0; i < kMaxExperts / 32; ++i)
-        if (i * 32 + lane >= p.experts) taken |= 1u << i;
     float mine = 0.f, chosen_sum = 0.f;
     int mine_id = 0;
+#pragma unroll 1
     for (int j = 0; j < p.top_k; ++j) {
-        // the lane's best: highest value, lowest index; NaN below everything
-        float best = 0.f;
-        int at = -1;
-#pragma unroll
-        for (int i = 0; i < kMaxExperts / 32; ++i) {
-            if (i * 32 >= p.experts) break;
-            if (!(taken >> i & 1) && (at < 0 || v[i] > best || (best != best && v[i] == v[i]))) best = v[i], at = i;
+        uint32_t k = 0, at = 0xffffffffu;
+#pragma unroll 4
+        for (int e = lane; e < p.experts; e += 32) {
+            const uint32_t v = keys[e];
+            if (v > k) k = v, at = e;
         }
-        // order as integers: value, then the lower index; 0 for a lane with nothing left
-        uint32_t key = 0;
-        if (at >= 0) {
-            const uint32_t u = __float_as_uint(best + 0.f);  // -0 and +0 are one value
-            key = best != best ? 1u : (u & 0x80000000u ? ~u : u | 0x80000000u);
-        }
-        const uint32_t high = __reduce_max_sync(0xffffffffu, key);
-        const uint32_t cand = key == high && at >= 0 ? (uint32_t)(at * 32 + lane) : 0xffffffffu;
-        const uint32_t e = __reduce_min_sync(0xffffffffu, cand);
-        if (cand == e) taken |= 1u << at;
-        const float lv = __shfl_sync(0xffffffffu, best, e & 31);
-        const float w = expf(lv - top) / sum;
+        const uint32_t high = __reduce_max_sync(0xffffffffu, k);
+        const uint32_t e = __reduce_min_sync(0xffffffffu, k == high ? at : 0xffffffffu);
+        if (e == at) keys[e] = 0;
+        const float w = expf(key_logit(high) - top) / sum;
         chosen_sum += w;
         if (lane == j) mine = w, mine_id = (int)e;
     }
     if (lane < p.top_k) {
-        float w = p.renormalize ? mine / chosen_sum : mine;
-        if (nan) w = __int_as_float(0x7FFFFFFF);
+        const float w = p.renormalize ? mine / chosen_sum : mine;
         R->id[t * p.top_k + lane] = (uint16_t)mine_id;
         R->weight[t * p.top_k + lane] = w;
         atomicOr(&R->mask[mine_id], 1u << t);
@@ -317,12 +319,13 @@ __device__ __forceinline__ void route_token(const Params& p, Routing* R, int t, 
 
 // Active experts in ascending order and the first row of each (one warp).
 __device__ __forceinline__ void list_experts(const Params& p, Routing* R, int lane) {
-    int n = 0, rows = 0;
+    int n = 0, rows = 0, most = 0;
     for (int e0 = 0; e0 < p.experts; e0 += 32) {
         const int e = e0 + lane;
         const int c = e < p.experts ? __popc(R->mask[e]) : 0;
         const uint32_t on = __ballot_sync(0xffffffffu, c > 0);
         if (on == 0) continue;
+        most = max(most, c);
         int pre = c;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
@@ -336,7 +339,8 @@ __device__ __forceinline__ void list_experts(const Params& p, Routing* R, int la
         n += __popc(on);
         rows += __shfl_sync(0xffffffffu, pre, 31);
     }
-    if (lane == 0) R->n_active = n;
+    most = __reduce_max_sync(0xffffffffu, most);
+    if (lane == 0) R->n_active = n, R->n_most = most;
 }
 
 // -------------------------------------------------------- unit sequences
@@ -347,15 +351,33 @@ __device__ __forceinline__ int owner(int total, int u) {
     return (int)((((int64_t)u + 1) * gridDim.x - 1) / total);
 }
 
+// own[i * pitch] (i < n) = the sum of a tile's pieces in CTA order.  Pieces lie
+// [CTA][at the tile's start: 1, later: 0][`size` floats], this thread's values
+// of them at `pieces` + i * pitch.
+__device__ __forceinline__ void join(float* own, int pitch, int n, const float* pieces, int64_t size, int total,
+                                     int first, int whole) {
+    const int c0 = owner(total, first), c1 = owner(total, first + whole - 1);
+#pragma unroll 2
+    for (int i = 0; i < n; ++i) {
+        float v = 0.f;
+#pragma unroll 4
+        for (int c = c0; c <= c1; ++c) {
+            const int from = cut(total, c);
+            if (from < cut(total, c + 1)) v += __ldcg(pieces + (c * 2 + (from > first ? 0 : 1)) * size + i * pitch);
+        }
+        own[i * pitch] = v;
+    }
+}
+
 struct Shared {
     Routing route;
-    uint64_t full[kMaxRing], empty[kMaxRing], sfull[kScaleSlots], sempty[kScaleSlots], tfull[2], tempty[2];
+    uint64_t full[kMaxRing], empty[kMaxRing], sfull[kScaleSlots], sempty[kScaleSlots], tfull[kMaxBufs], tempty[kMaxBufs];
     float scale[kScaleSlots][kMaxTokens + 2];  // token (or row) scales, the two weight scales
     uint32_t taddr;
     uint64_t h_arrived;              // the CTA's last h is written and its arrival posted
     unsigned long long h_target;     // the barrier round of that arrival
     int dead, last;
-    uint32_t max_bits[4][kMaxTokens];
+    __align__(16) uint32_t max_bits[kMaxTokens][4];
 };
 
 __device__ __forceinline__ void bar_promotion() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
@@ -400,7 +422,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
             mbar_init(&S->sfull[i], 32);
             mbar_init(&S->sempty[i], 8);
         }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < kMaxBufs; ++i) {
             mbar_init(&S->tfull[i], 1);
             mbar_init(&S->tempty[i], 8);
         }
@@ -409,14 +431,19 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
     }
     for (int e = threadIdx.x; e < p.experts; e += kThreads) R->mask[e] = 0;
     // ---- phase 0: logits and the digits of x
-    {
-        const int groups = (p.tokens + 3) / 4, n_logits = p.experts * groups, n_all = n_logits + p.tokens * nkb1;
-        for (int u = blockIdx.x + gridDim.x * warp; u < n_all; u += gridDim.x * kWarps) {
-            if (u < n_logits)
-                logits_unit(p, u / groups, u % groups * 4, lane);
-            else
-                x_digits_unit(p, (u - n_logits) / nkb1, (u - n_logits) % nkb1, lane);
+    float* share = reinterpret_cast<float*>(ring);  // [kWarps][32], before the ring is in use
+    for (int u = gridDim.x - 1 - blockIdx.x + gridDim.x * warp; u < p.tokens * nkb1; u += gridDim.x * kWarps)
+        x_digits_unit(p, u / nkb1, u % nkb1, lane);
+    for (int e = blockIdx.x; e < p.experts; e += gridDim.x) {
+        share[warp * 32 + lane] = logits_share(p, e, warp, lane);
+        __syncthreads();
+        if (threadIdx.x < p.tokens) {
+            float v = 0.f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) v += share[w * 32 + threadIdx.x];
+            p.logits[threadIdx.x * p.experts + e] = v;
         }
+        __syncthreads();
     }
     fence_proxy_all();  // the digits are read by TMA
     tc_fence_before();
@@ -429,7 +456,11 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
 
     // ---- routing, by every CTA for itself
     if (!*dead) {
-        for (int t = warp; t < p.tokens; t += kWarps) route_token(p, R, t, lane);
+        uint32_t* keys = reinterpret_cast<uint32_t*>(ring) + warp * p.experts;
+        for (int t = warp; t < p.tokens; t += kWarps) {
+            route_token(p, R, keys, t, lane);
+            __syncwarp();
+        }
     }
     __syncthreads();
     if (warp == 0) list_experts(p, R, lane);
@@ -443,44 +474,64 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
     __syncthreads();
 
     const int n_act = *dead ? 0 : R->n_active;
+    // columns of an accumulator: what the expert with the most tokens needs
+    const uint32_t cols = b_rows(*dead ? 1 : R->n_most);
+    uint32_t bufs = kMaxBufs, bufs_log = 3;
+    while (bufs * 2 * cols > 512) bufs /= 2, --bufs_log;
     const int total1 = n_act * p.tiles_i * nkb1, total2 = p.tiles_h * n_act * nkb2;
     const int u1a = cut(total1, blockIdx.x), u1b = cut(total1, blockIdx.x + 1);
     const int u2a = cut(total2, blockIdx.x), u2b = cut(total2, blockIdx.x + 1);
+
+    // The ring's memory was written by threads; TMA writes it from here on.
+    // (Every thread's fence, then the barrier above all roles' first copies.)
+    fence_proxy_all();
+    __syncthreads();
 
     if (warp == 0) {  // ---------------------------------------------- weights
         if (lane == 0) {
             int st = 0, ph = 0;
             bool alive = true;
-            for (int u = u1a; u < u1b && alive; ++u) {
-                const int tile = u / nkb1, kb = u - tile * nkb1, a = tile / p.tiles_i, ti = tile - a * p.tiles_i;
-                const int e = R->active[a];
+            if (u1a < u1b) {
+                int kb = u1a % nkb1, ti = u1a / nkb1 % p.tiles_i, a = u1a / nkb1 / p.tiles_i, e = R->active[a];
+                for (int u = u1a; u < u1b && alive; ++u) {
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    if (!(alive = wait_alive(&S->empty[st], ph ^ 1, dead))) break;
-                    mbar_expect_tx(&S->full[st], kTileBytes);
-                    tma_load_3d(ring + st * p.stage_bytes, &map_w13, &S->full[st], kb * kBlockK, ti * 128, 2 * e + half);
-                    if (++st == p.stages) st = 0, ph ^= 1;
+                    for (int half = 0; half < 2; ++half) {
+                        if (!(alive = wait_alive(&S->empty[st], ph ^ 1, dead))) break;
+                        mbar_expect_tx(&S->full[st], kTileBytes);
+                        tma_load_3d(ring + st * p.stage_bytes, &map_w13, &S->full[st], kb * kBlockK, ti * 128, 2 * e + half);
+                        if (++st == p.stages) st = 0, ph ^= 1;
+                    }
+                    if (++kb == nkb1) {
+                        kb = 0;
+                        if (++ti == p.tiles_i && ++a < n_act) e = R->active[a];
+                        if (ti == p.tiles_i) ti = 0;
+                    }
                 }
             }
-            for (int u = u2a; u < u2b && alive; ++u) {
-                const int run = u / nkb2, kb = u - run * nkb2, rt = run / n_act, a = run - rt * n_act;
-                if (!(alive = wait_alive(&S->empty[st], ph ^ 1, dead))) break;
-                mbar_expect_tx(&S->full[st], kTileBytes);
-                tma_load_3d(ring + st * p.stage_bytes, &map_w2, &S->full[st], kb * kBlockK, rt * 128, R->active[a]);
-                if (++st == p.stages) st = 0, ph ^= 1;
+            if (u2a < u2b) {
+                int kb = u2a % nkb2, a = u2a / nkb2 % n_act, rt = u2a / nkb2 / n_act;
+                for (int u = u2a; u < u2b && alive; ++u) {
+                    if (!(alive = wait_alive(&S->empty[st], ph ^ 1, dead))) break;
+                    mbar_expect_tx(&S->full[st], kTileBytes);
+                    tma_load_3d(ring + st * p.stage_bytes, &map_w2, &S->full[st], kb * kBlockK, rt * 128, R->active[a]);
+                    if (++st == p.stages) st = 0, ph ^= 1;
+                    if (++kb == nkb2) {
+                        kb = 0;
+                        if (++a == n_act) a = 0, ++rt;
+                    }
+                }
             }
             if (!alive) let_copies_land();
         }
     } else if (warp == 1) {  // ---------------------------- matrix instructions
         if (lane == 0) {
+            const uint32_t idesc = instr_desc(0, 0, 128, cols);
             int st = 0, ph = 0;
             uint32_t it = 0;
             bool alive = true;
             for (int u = u1a; u < u1b && alive; ++u, ++it) {
-                const int a = u / nkb1 / p.tiles_i, n = __popc(R->mask[R->active[a]]);
-                const uint32_t idesc = instr_desc(0, 0, 128, b_rows(n));
-                const int buf = it & 1;
-                alive = wait_alive(&S->tempty[buf], ((it >> 1) & 1) ^ 1, dead);
+                const int buf = it & (bufs - 1);
+                alive = wait_alive(&S->tempty[buf], ((it >> bufs_log) & 1) ^ 1, dead);
                 uint32_t b = 0, first = 0;
 #pragma unroll
                 for (int half = 0; half < 2 && alive; ++half) {
@@ -488,7 +539,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
                     tc_fence_after();
                     const uint32_t at = smem_u32(ring + st * p.stage_bytes);
                     if (half == 0) b = at + kTileBytes, first = st;  // the up tile shares the gate tile's digits
-                    mma_block(taddr + buf * 256 + half * 128, at, b, idesc);
+                    mma_block(taddr + (buf * 2 + half) * cols, at, b, idesc);
                     if (half == 1) {
                         mma_commit(&S->empty[first]);
                         mma_commit(&S->empty[st]);
@@ -498,14 +549,12 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
                 }
             }
             for (int u = u2a; u < u2b && alive; ++u, ++it) {
-                const int run = u / nkb2, a = run % n_act, n = __popc(R->mask[R->active[a]]);
-                const uint32_t idesc = instr_desc(0, 0, 128, b_rows(n));
-                const int buf = it & 1;
-                alive = wait_alive(&S->tempty[buf], ((it >> 1) & 1) ^ 1, dead) && wait_alive(&S->full[st], ph, dead);
+                const int buf = it & (bufs - 1);
+                alive = wait_alive(&S->tempty[buf], ((it >> bufs_log) & 1) ^ 1, dead) && wait_alive(&S->full[st], ph, dead);
                 if (!alive) break;
                 tc_fence_after();
                 const uint32_t at = smem_u32(ring + st * p.stage_bytes);
-                mma_block(taddr + buf * 256, at, at + kTileBytes, idesc);
+                mma_block(taddr + buf * 2 * cols, at, at + kTileBytes, idesc);
                 mma_commit(&S->empty[st]);
                 mma_commit(&S->tfull[buf]);
                 if (++st == p.stages) st = 0, ph ^= 1;
@@ -516,29 +565,33 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
         int st = 0, ph = 0;
         uint32_t it = 0;
         bool alive = true;
-        for (int u = u1a; u < u1b && alive; ++u, ++it) {
-            const int tile = u / nkb1, kb = u - tile * nkb1, a = tile / p.tiles_i, ti = tile - a * p.tiles_i;
-            const int e = R->active[a], n = __popc(R->mask[e]);
-            const int t = lane < n ? R->row_token[R->base[e] + lane] : 0, slot = it % kScaleSlots;
-            alive = __all_sync(0xffffffffu, wait_alive(&S->sempty[slot], ((it / kScaleSlots) & 1) ^ 1, dead) &&
-                                                wait_alive(&S->empty[st], ph ^ 1, dead));
-            if (!alive) break;
-            if (lane < n) cp_async4(&S->scale[slot][lane], p.sx + t * nkb1 + kb, true);
-            if (lane < 2)
-                cp_async4(&S->scale[slot][kMaxTokens + lane],
-                          p.s13 + (((int64_t)e * 2 + lane) * p.tiles_i + ti) * nkb1 + kb, true);
-            cp_async_arrive(&S->sfull[slot]);
-            if (lane == 0) mbar_expect_tx(&S->full[st], (uint32_t)n * kDigits * kBlockK);
-            __syncwarp();
-            if (lane < n)
-                tma_load_2d(ring + st * p.stage_bytes + kTileBytes + lane * kDigits * kBlockK, &map_x, &S->full[st],
-                            kb * kBlockK, t * kDigits);
-            if (++st == p.stages) st = 0, ph ^= 1;
-            // the up tile's stage brings no digits of its own
-            alive = __all_sync(0xffffffffu, wait_alive(&S->empty[st], ph ^ 1, dead));
-            if (!alive) break;
-            if (lane == 0) mbar_arrive(&S->full[st]);
-            if (++st == p.stages) st = 0, ph ^= 1;
+        for (int u = u1a; u < u1b && alive;) {
+            const int tile = u / nkb1, k0 = u - tile * nkb1, k1 = min(nkb1, k0 + u1b - u);
+            const int a = tile / p.tiles_i, ti = tile - a * p.tiles_i, e = R->active[a], n = __popc(R->mask[e]);
+            const int t = lane < n ? R->row_token[R->base[e] + lane] : 0;
+            const float* sx = p.sx + t * nkb1;
+            const float* sw = p.s13 + (((int64_t)e * 2 + (lane & 1)) * p.tiles_i + ti) * nkb1;
+            for (int kb = k0; kb < k1; ++kb, ++it) {
+                const int slot = it % kScaleSlots;
+                alive = __all_sync(0xffffffffu, wait_alive(&S->sempty[slot], ((it / kScaleSlots) & 1) ^ 1, dead) &&
+                                                    wait_alive(&S->empty[st], ph ^ 1, dead));
+                if (!alive) break;
+                if (lane == 0) mbar_expect_tx(&S->full[st], (uint32_t)n * kDigits * kBlockK);
+                __syncwarp();
+                if (lane < n)
+                    tma_load_2d(ring + st * p.stage_bytes + kTileBytes + lane * kDigits * kBlockK, &map_x, &S->full[st],
+                                kb * kBlockK, t * kDigits);
+                if (lane < n) cp_async4(&S->scale[slot][lane], sx + kb, true);
+                if (lane < 2) cp_async4(&S->scale[slot][kMaxTokens + lane], sw + kb, true);
+                cp_async_arrive(&S->sfull[slot]);
+                if (++st == p.stages) st = 0, ph ^= 1;
+                // the up tile's stage brings no digits of its own
+                alive = __all_sync(0xffffffffu, wait_alive(&S->empty[st], ph ^ 1, dead));
+                if (!alive) break;
+                if (lane == 0) mbar_arrive(&S->full[st]);
+                if (++st == p.stages) st = 0, ph ^= 1;
+            }
+            u += k1 - k0;
         }
         // every h of the grid has to be there
         if (u2a < u2b && alive) {
@@ -547,22 +600,27 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
             alive = __all_sync(0xffffffffu, ok);
             fence_proxy_all();
         }
-        for (int u = u2a; u < u2b && alive; ++u, ++it) {
-            const int run = u / nkb2, kb = u - run * nkb2, rt = run / n_act, a = run - rt * n_act;
-            const int e = R->active[a], n = __popc(R->mask[e]), row0 = R->base[e], slot = it % kScaleSlots;
-            alive = __all_sync(0xffffffffu, wait_alive(&S->sempty[slot], ((it / kScaleSlots) & 1) ^ 1, dead) &&
-                                                wait_alive(&S->empty[st], ph ^ 1, dead));
-            if (!alive) break;
-            if (lane < n) cp_async4(&S->scale[slot][lane], p.sh + (int64_t)(row0 + lane) * nkb2 + kb, true);
-            if (lane == 0)
-                cp_async4(&S->scale[slot][kMaxTokens], p.s2 + ((int64_t)e * p.tiles_h + rt) * nkb2 + kb, true);
-            cp_async_arrive(&S->sfull[slot]);
-            if (lane == 0) mbar_expect_tx(&S->full[st], (uint32_t)n * kDigits * kBlockK);
-            __syncwarp();
-            if (lane < n)
-                tma_load_2d(ring + st * p.stage_bytes + kTileBytes + lane * kDigits * kBlockK, &map_h, &S->full[st],
-                            kb * kBlockK, (row0 + lane) * kDigits);
-            if (++st == p.stages) st = 0, ph ^= 1;
+        for (int u = u2a; u < u2b && alive;) {
+            const int run = u / nkb2, k0 = u - run * nkb2, k1 = min(nkb2, k0 + u2b - u), rt = run / n_act;
+            const int e = R->active[run - rt * n_act], n = __popc(R->mask[e]), row = R->base[e] + (lane < n ? lane : 0);
+            const float* sh = p.sh + (int64_t)row * nkb2;
+            const float* sw = p.s2 + ((int64_t)e * p.tiles_h + rt) * nkb2;
+            for (int kb = k0; kb < k1; ++kb, ++it) {
+                const int slot = it % kScaleSlots;
+                alive = __all_sync(0xffffffffu, wait_alive(&S->sempty[slot], ((it / kScaleSlots) & 1) ^ 1, dead) &&
+                                                    wait_alive(&S->empty[st], ph ^ 1, dead));
+                if (!alive) break;
+                if (lane == 0) mbar_expect_tx(&S->full[st], (uint32_t)n * kDigits * kBlockK);
+                __syncwarp();
+                if (lane < n)
+                    tma_load_2d(ring + st * p.stage_bytes + kTileBytes + lane * kDigits * kBlockK, &map_h, &S->full[st],
+                                kb * kBlockK, row * kDigits);
+                if (lane < n) cp_async4(&S->scale[slot][lane], sh + kb, true);
+                if (lane == 0) cp_async4(&S->scale[slot][kMaxTokens], sw + kb, true);
+                cp_async_arrive(&S->sfull[slot]);
+                if (++st == p.stages) st = 0, ph ^= 1;
+            }
+            u += k1 - k0;
         }
     } else if (warp >= 4) {  // ------------------------------------- promotion
         const int group = (warp - 4) / 4, r = (warp & 3) * 32 + lane;
@@ -577,7 +635,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
             const int slot = it % kScaleSlots;
             if (alive)
                 alive = __all_sync(0xffffffffu, wait_alive(&S->sfull[slot], (it / kScaleSlots) & 1, dead) &&
-                                                    wait_alive(&S->tfull[it & 1], (it >> 1) & 1, dead));
+                                                    wait_alive(&S->tfull[it & (bufs - 1)], (it >> bufs_log) & 1, dead));
             tc_fence_after();
             return S->scale[slot];
         };
@@ -585,7 +643,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
             tc_fence_before();
             __syncwarp();
             if (lane == 0) {
-                mbar_arrive(&S->tempty[it & 1]);
+                mbar_arrive(&S->tempty[it & (bufs - 1)]);
                 mbar_arrive(&S->sempty[it % kScaleSlots]);
             }
             ++it;
@@ -617,65 +675,45 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
                 const float sw = sc[kMaxTokens + group];
 #pragma unroll
                 for (int b = 0; b < 8; ++b)
-                    if (4 * b < n) promote4(acc[b], lanes + (it & 1) * 256 + group * 128 + b * 16, sc + 4 * b, sw);
+                    if (4 * b < n) promote4(acc[b], lanes + ((it & (bufs - 1)) * 2 + group) * cols + b * 16, sc + 4 * b, sw);
                 unit_done();
             }
+            // From here on in shared memory, token by token: [token][gate, up rows]
+            float* own = sums + group * 128 + r;
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+                if (i < n) own[i * 256] = acc[i / 4][i % 4];
             bool mine = len == nkb1;
             if (!mine) {  // a piece: at the tile's start (then the CTA's last tile) or not (then its first)
                 float* dst = p.part1 + ((int64_t)(blockIdx.x * 2 + (k0 > 0 ? 0 : 1)) * p.tokens) * 256 + group * 128 + r;
-#pragma unroll
-                for (int i = 0; i < 32; ++i)
-                    if (i < n) __stcg(dst + i * 256, acc[i / 4][i % 4]);
-                if ((mine = is_last(p.cnt1 + tile, len, nkb1))) {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) acc[i / 4][i % 4] = 0.f;
-                    const int t0 = tile * nkb1, c1 = owner(total1, t0 + nkb1 - 1);
-                    for (int c = owner(total1, t0); c <= c1; ++c) {
-                        const int ca = cut(total1, c);
-                        if (ca == cut(total1, c + 1)) continue;
-                        const float* src =
-                            p.part1 + ((int64_t)(c * 2 + (ca > t0 ? 0 : 1)) * p.tokens) * 256 + group * 128 + r;
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if (i < n) acc[i / 4][i % 4] += __ldcg(src + i * 256);
-                    }
-                }
+#pragma unroll 2
+                for (int i = 0; i < n; ++i) __stcg(dst + i * 256, own[i * 256]);
+                if ((mine = is_last(p.cnt1 + tile, len, nkb1)))
+                    join(own, 256, n, p.part1 + group * 128 + r, (int64_t)p.tokens * 256, total1, tile * nkb1, nkb1);
             }
-            if (mine) {  // h = silu(gate) * up, and its digits
-                if (group == 1) {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        if (i < n) sums[i * 128 + r] = acc[i / 4][i % 4];
+            if (mine) {  // h = silu(gate) * up, and its digits; group g takes the tokens of its parity
+                bar_promotion();
+#pragma unroll 1
+                for (int i = group; i < n; i += 2) {
+                    const float g = sums[i * 256 + r], h = g / (1.f + expf(-g)) * sums[i * 256 + 128 + r];
+                    sums[i * 256 + r] = h;
+                    const uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(h) & 0x7FFFFFFFu);
+                    if (lane == 0) S->max_bits[i][warp & 3] = m;
                 }
                 bar_promotion();
-                if (group == 0) {
+#pragma unroll 1
+                for (int i = group; i < n; i += 2) {
+                    const uint4 m = *reinterpret_cast<const uint4*>(S->max_bits[i]);
+                    float f;
+                    const float s = digit_scale(max(max(m.x, m.y), max(m.z, m.w)), &f);
+                    const uint32_t d = digits_of(sums[i * 256 + r] * f);
+                    uint8_t* dst = p.hq + (int64_t)(row0 + i) * kDigits * p.ipad + ti * 128 + r;
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        if (i < n) {
-                            const float g = acc[i / 4][i % 4], h = g / (1.f + expf(-g)) * sums[i * 128 + r];
-                            acc[i / 4][i % 4] = h;
-                            const uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(h) & 0x7FFFFFFFu);
-                            if (lane == 0) S->max_bits[warp & 3][i] = m;
-                        }
-                    }
-                    asm volatile("bar.sync 2, 128;" ::: "memory");
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        if (i < n) {
-                            float f;
-                            const float s = digit_scale(max(max(S->max_bits[0][i], S->max_bits[1][i]),
-                                                            max(S->max_bits[2][i], S->max_bits[3][i])),
-                                                        &f);
-                            const uint32_t d = digits_of(acc[i / 4][i % 4] * f);
-                            uint8_t* dst = p.hq + (int64_t)(row0 + i) * kDigits * p.ipad + ti * 128 + r;
-#pragma unroll
-                            for (int q = 0; q < kDigits; ++q) dst[(int64_t)q * p.ipad] = (uint8_t)(d >> (8 * q));
-                            if (r == 0) p.sh[(int64_t)(row0 + i) * nkb2 + ti] = s;
-                        }
-                    }
+                    for (int q = 0; q < kDigits; ++q) dst[(int64_t)q * p.ipad] = (uint8_t)(d >> (8 * q));
+                    if (r == 0) p.sh[(int64_t)(row0 + i) * nkb2 + ti] = s;
                 }
-                bar_promotion();  // `sums` is read
             }
+            bar_promotion();  // `sums` is read
             u += len;
         }
         __threadfence();
@@ -702,7 +740,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         const int b = 2 * j + group;
-                        if (4 * b < n) promote4(acc[j], lanes + (it & 1) * 256 + b * 16, sc + 4 * b, sw);
+                        if (4 * b < n) promote4(acc[j], lanes + (it & (bufs - 1)) * 2 * cols + b * 16, sc + 4 * b, sw);
                     }
                     unit_done();
                 }
@@ -716,30 +754,23 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
                 v += run;
             }
             bar_promotion();
-            // the two groups' sums; group g finishes the tokens of its parity
+            // the two groups' sums meet; group g finishes the tokens of its parity
+            float* both = sums + r;
+#pragma unroll 2
+            for (int i = group; i < p.tokens; i += 2) both[i * 128] += both[(p.tokens + i) * 128];
             bool mine = len == per;
-            const float* other = sums + r;
             if (!mine) {
                 float* dst = p.part2 + ((int64_t)(blockIdx.x * 2 + (k0 > 0 ? 0 : 1)) * p.tokens) * 128 + r;
-                for (int t = group; t < p.tokens; t += 2)
-                    __stcg(dst + t * 128, other[t * 128] + other[(p.tokens + t) * 128]);
-                mine = is_last(p.cnt2 + rt, len, per);
+#pragma unroll 2
+                for (int i = group; i < p.tokens; i += 2) __stcg(dst + i * 128, both[i * 128]);
+                if ((mine = is_last(p.cnt2 + rt, len, per)))
+                    join(both + group * 128, 256, (p.tokens - group + 1) / 2, p.part2 + group * 128 + r,
+                         (int64_t)p.tokens * 128, total2, rt * per, per);
             }
             if (mine && rt * 128 + r < p.hidden) {
-                const int t0 = rt * per, c0 = owner(total2, t0), c1 = owner(total2, t0 + per - 1);
-                for (int t = group; t < p.tokens; t += 2) {
-                    float v = 0.f;
-                    if (len == per) {
-                        v = other[t * 128] + other[(p.tokens + t) * 128];
-                    } else {
-                        for (int c = c0; c <= c1; ++c) {
-                            const int ca = cut(total2, c);
-                            if (ca == cut(total2, c + 1)) continue;
-                            v += __ldcg(p.part2 + ((int64_t)(c * 2 + (ca > t0 ? 0 : 1)) * p.tokens + t) * 128 + r);
-                        }
-                    }
-                    store_out(p.y, t * p.ldy + rt * 128 + r, p.bf16 ? kBF16 : kF16, v);
-                }
+#pragma unroll 1
+                for (int i = group; i < p.tokens; i += 2)
+                    store_out(p.y, i * p.ldy + rt * 128 + r, p.bf16 ? kBF16 : kF16, both[i * 128]);
             }
             bar_promotion();  // `sums` is read
             u += len;
