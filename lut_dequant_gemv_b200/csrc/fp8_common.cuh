@@ -22,6 +22,7 @@ namespace sqz {
 namespace f8 {
 
 using tc::fence_mbar_init;
+using tc::fence_proxy_async;
 using tc::mbar_arrive;
 using tc::mbar_expect_tx;
 using tc::mbar_init;

@@ -348,6 +348,7 @@ __global__ void __launch_bounds__(224) fp8_gemm_few_kernel(const __grid_constant
             if (++st == p.stages) st = 0, ph ^= 1;
         }
     }
+    __syncwarp();  // one lane ran the role: the barrier counts whole warps
     __syncthreads();
     tc_fence_after();
     if (warp == 1) tmem_dealloc(taddr, S::kTmemCols);
@@ -559,6 +560,7 @@ __global__ void __launch_bounds__(320, 1) fp8_gemm_many_kernel(const __grid_cons
             }
         }
     }
+    __syncwarp();  // one lane ran the role: the barrier counts whole warps
     __syncthreads();
     tc_fence_after();
     if (warp == 1) tmem_dealloc(taddr, S::kTmemCols);

@@ -61,6 +61,7 @@ constexpr int kMaxRing = 12;
 constexpr int kScaleSlots = 8;
 constexpr int kMaxBufs = 8;  // accumulators in tensor memory (a power of two; see kernels_fp8.cuh)
 constexpr int kDigits = 4;
+constexpr int kMaxGrid = 256;  // CTAs (one per SM)
 
 // Start of the caller's workspace.  Zero before the first call; every call
 // leaves the tile counters zero and the barrier counter a multiple of the
@@ -101,6 +102,12 @@ struct Params {
 };
 
 __host__ __device__ inline int b_rows(int tokens) { return (kDigits * tokens + 15) / 16 * 16; }
+
+// Shared memory of the logits' shares and, later, of the warps' logit keys.
+__host__ __device__ inline int scratch_bytes(int tokens, int experts) {
+    const int keys = (tokens < kWarps ? tokens : kWarps) * experts * 4, share = kWarps * 32 * 4;
+    return ((keys > share ? keys : share) + 127) / 128 * 128;
+}
 
 __device__ __forceinline__ float load_x(const uint16_t* p, bool bf16) {
     const uint16_t h = __ldg(p);
@@ -183,11 +190,13 @@ __device__ __forceinline__ void load_x8(const uint16_t* row, int c, const Params
     }
 }
 
-// The logits of expert e for every token: the warp's share of the columns
-// (runs of 256, 8 a lane), then the lanes' sums; lane t returns token t's.
+// The logits of expert e for tokens [t_begin, t_end): the warp's share of the
+// columns (runs of 256, 8 a lane), then the lanes' sums; lane t returns token
+// t's.
 // The expert's row is held in registers (two runs at a time), so a token costs
 // its own loads only; four tokens' sums cross the lanes together.
-__device__ __forceinline__ float logits_share(const Params& p, int e, int warp, int lane) {
+__device__ __forceinline__ float logits_share(const Params& p, int e, int t_begin, int t_end, int warp,
+                                              int lane) {
     const uint16_t* r = p.router + (int64_t)e * p.ld_router;
     float mine = 0.f;
     for (int c0 = warp * 256; c0 < p.hidden; c0 += 2 * kWarps * 256) {
@@ -195,12 +204,12 @@ __device__ __forceinline__ float logits_share(const Params& p, int e, int warp, 
         float ra[8], rb[8];
         load_x8(r, ca, p, ra);
         load_x8(r, cb, p, rb);
-#pragma unroll 1
-        for (int t0 = 0; t0 < p.tokens; t0 += 4) {
+#pragma unroll 2
+        for (int t0 = t_begin; t0 < t_end; t0 += 4) {
             float s[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const uint16_t* x = p.x + (int64_t)min(t0 + i, p.tokens - 1) * p.ldx;
+                const uint16_t* x = p.x + (int64_t)min(t0 + i, t_end - 1) * p.ldx;
                 float xa[8], xb[8];
                 load_x8(x, ca, p, xa);
                 load_x8(x, cb, p, xb);
@@ -317,7 +326,8 @@ __device__ __forceinline__ void route_token(const Params& p, Routing* R, uint32_
     }
 }
 
-// Active experts in ascending order and the first row of each (one warp).
+// Active experts in ascending order, the first row of each, and the rows'
+// tokens and weights (one warp).
 __device__ __forceinline__ void list_experts(const Params& p, Routing* R, int lane) {
     int n = 0, rows = 0, most = 0;
     for (int e0 = 0; e0 < p.experts; e0 += 32) {
@@ -341,32 +351,57 @@ __device__ __forceinline__ void list_experts(const Params& p, Routing* R, int la
     }
     most = __reduce_max_sync(0xffffffffu, most);
     if (lane == 0) R->n_active = n, R->n_most = most;
+    __syncwarp();
+    for (int i = lane; i < p.tokens * p.top_k; i += 32) {
+        const int t = i / p.top_k, e = R->id[i];
+        const int row = R->base[e] + __popc(R->mask[e] & ((1u << t) - 1));
+        R->row_token[row] = (uint8_t)t;
+        R->row_weight[row] = R->weight[i];
+    }
 }
 
 // -------------------------------------------------------- unit sequences
-// `total` units cut evenly: CTA c has [begin(c), begin(c + 1)).
-__device__ __forceinline__ int cut(int total, int c) { return (int)((int64_t)total * c / gridDim.x); }
+// `total` units cut evenly: CTA c has [cuts[c], cuts[c + 1]).  The table is in
+// shared memory (a 64-bit division each, once).
+__device__ __forceinline__ void make_cuts(int* cuts, int total) {
+    for (int c = threadIdx.x; c <= gridDim.x; c += kThreads) cuts[c] = (int)((int64_t)total * c / gridDim.x);
+}
 // The CTA that has unit u.
 __device__ __forceinline__ int owner(int total, int u) {
     return (int)((((int64_t)u + 1) * gridDim.x - 1) / total);
 }
 
-// own[i * pitch] (i < n) = the sum of a tile's pieces in CTA order.  Pieces lie
-// [CTA][at the tile's start: 1, later: 0][`size` floats], this thread's values
-// of them at `pieces` + i * pitch.
-__device__ __forceinline__ void join(float* own, int pitch, int n, const float* pieces, int64_t size, int total,
-                                     int first, int whole) {
-    const int c0 = owner(total, first), c1 = owner(total, first + whole - 1);
-#pragma unroll 2
-    for (int i = 0; i < n; ++i) {
-        float v = 0.f;
-#pragma unroll 4
-        for (int c = c0; c <= c1; ++c) {
-            const int from = cut(total, c);
-            if (from < cut(total, c + 1)) v += __ldcg(pieces + (c * 2 + (from > first ? 0 : 1)) * size + i * pitch);
+// Four consecutive floats of a tile's sum: its pieces added in CTA order.
+// Pieces lie [CTA][at the tile's start: 1, later: 0][size floats]; `at` is the
+// place in a piece.  All the loads of a group of eight pieces are in flight
+// together.
+__device__ __forceinline__ float4 join4(const float* pieces, int64_t size, int at, const int* cuts, int c0, int c1,
+                                        int first) {
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int cb = c0; cb <= c1; cb += 8) {
+        float4 w[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int c = min(cb + j, c1), from = cuts[c];
+            w[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (cb + j <= c1 && from < cuts[c + 1])
+                w[j] = __ldcg(reinterpret_cast<const float4*>(pieces + (c * 2 + (from > first ? 0 : 1)) * size + at));
         }
-        own[i * pitch] = v;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v.x += w[j].x, v.y += w[j].y, v.z += w[j].z, v.w += w[j].w;
     }
+    return v;
+}
+
+// Four consecutive columns of y (hidden is a multiple of 16: all or none).
+__device__ __forceinline__ void store_y(const Params& p, int token, int col, const float4& v) {
+    if (col >= p.hidden) return;
+    const int64_t at = token * p.ldy + col;
+    const int type = p.bf16 ? kBF16 : kF16;
+    store_out(p.y, at, type, v.x);
+    store_out(p.y, at + 1, type, v.y);
+    store_out(p.y, at + 2, type, v.z);
+    store_out(p.y, at + 3, type, v.w);
 }
 
 struct Shared {
@@ -377,6 +412,7 @@ struct Shared {
     uint64_t h_arrived;              // the CTA's last h is written and its arrival posted
     unsigned long long h_target;     // the barrier round of that arrival
     int dead, last;
+    int cuts[2][kMaxGrid + 1];       // units of the two products by CTA
     __align__(16) uint32_t max_bits[kMaxTokens][4];
 };
 
@@ -405,7 +441,8 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
     extern __shared__ uint8_t smem_raw[];
     uint8_t* ring = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
     float* sums = reinterpret_cast<float*>(ring + p.stages * p.stage_bytes);  // [2][tokens][128]
-    Shared* S = reinterpret_cast<Shared*>(sums + 2 * p.tokens * 128);
+    uint8_t* scratch = reinterpret_cast<uint8_t*>(sums + 2 * p.tokens * 128);  // phase 0 and routing
+    Shared* S = reinterpret_cast<Shared*>(scratch + scratch_bytes(p.tokens, p.experts));
     Routing* R = &S->route;
     volatile int* dead = &S->dead;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -431,17 +468,23 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
     }
     for (int e = threadIdx.x; e < p.experts; e += kThreads) R->mask[e] = 0;
     // ---- phase 0: logits and the digits of x
-    float* share = reinterpret_cast<float*>(ring);  // [kWarps][32], before the ring is in use
+    float* share = reinterpret_cast<float*>(scratch);  // [kWarps][32]
     for (int u = gridDim.x - 1 - blockIdx.x + gridDim.x * warp; u < p.tokens * nkb1; u += gridDim.x * kWarps)
         x_digits_unit(p, u / nkb1, u % nkb1, lane);
-    for (int e = blockIdx.x; e < p.experts; e += gridDim.x) {
-        share[warp * 32 + lane] = logits_share(p, e, warp, lane);
+    // an expert's tokens in as many groups (of whole fours) as there are CTAs for
+    int groups = max(1, min((p.tokens + 3) / 4, (int)gridDim.x / p.experts));
+    const int per_group = ((p.tokens + 3) / 4 + groups - 1) / groups * 4;
+    groups = (p.tokens + per_group - 1) / per_group;
+    for (int u = blockIdx.x; u < p.experts * groups; u += gridDim.x) {
+        const int e = u / groups, t0 = (u - e * groups) * per_group, t1 = min(t0 + per_group, p.tokens);
+        share[warp * 32 + lane] = logits_share(p, e, t0, t1, warp, lane);
         __syncthreads();
-        if (threadIdx.x < p.tokens) {
+        const int t = t0 + threadIdx.x;
+        if (t < t1) {
             float v = 0.f;
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) v += share[w * 32 + threadIdx.x];
-            p.logits[threadIdx.x * p.experts + e] = v;
+            for (int w = 0; w < kWarps; ++w) v += share[w * 32 + t];
+            p.logits[t * p.experts + e] = v;
         }
         __syncthreads();
     }
@@ -452,11 +495,10 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
     const uint32_t taddr = S->taddr;
     if (threadIdx.x == 0) grid_wait(p.head, grid_arrive(p.head), dead);
     __syncthreads();
-    fence_proxy_all();
 
     // ---- routing, by every CTA for itself
     if (!*dead) {
-        uint32_t* keys = reinterpret_cast<uint32_t*>(ring) + warp * p.experts;
+        uint32_t* keys = reinterpret_cast<uint32_t*>(scratch) + warp * p.experts;
         for (int t = warp; t < p.tokens; t += kWarps) {
             route_token(p, R, keys, t, lane);
             __syncwarp();
@@ -465,13 +507,6 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
     __syncthreads();
     if (warp == 0) list_experts(p, R, lane);
     __syncthreads();
-    for (int i = threadIdx.x; i < p.tokens * p.top_k; i += kThreads) {
-        const int t = i / p.top_k, e = R->id[i];
-        const int row = R->base[e] + __popc(R->mask[e] & ((1u << t) - 1));
-        R->row_token[row] = (uint8_t)t;
-        R->row_weight[row] = R->weight[i];
-    }
-    __syncthreads();
 
     const int n_act = *dead ? 0 : R->n_active;
     // columns of an accumulator: what the expert with the most tokens needs
@@ -479,13 +514,11 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
     uint32_t bufs = kMaxBufs, bufs_log = 3;
     while (bufs * 2 * cols > 512) bufs /= 2, --bufs_log;
     const int total1 = n_act * p.tiles_i * nkb1, total2 = p.tiles_h * n_act * nkb2;
-    const int u1a = cut(total1, blockIdx.x), u1b = cut(total1, blockIdx.x + 1);
-    const int u2a = cut(total2, blockIdx.x), u2b = cut(total2, blockIdx.x + 1);
-
-    // The ring's memory was written by threads; TMA writes it from here on.
-    // (Every thread's fence, then the barrier above all roles' first copies.)
-    fence_proxy_all();
+    make_cuts(S->cuts[0], total1);
+    make_cuts(S->cuts[1], total2);
     __syncthreads();
+    const int u1a = S->cuts[0][blockIdx.x], u1b = S->cuts[0][blockIdx.x + 1];
+    const int u2a = S->cuts[1][blockIdx.x], u2b = S->cuts[1][blockIdx.x + 1];
 
     if (warp == 0) {  // ---------------------------------------------- weights
         if (lane == 0) {
@@ -565,6 +598,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
         int st = 0, ph = 0;
         uint32_t it = 0;
         bool alive = true;
+        fence_proxy_all();  // the digits of x were written by threads before the grid's barrier
         for (int u = u1a; u < u1b && alive;) {
             const int tile = u / nkb1, k0 = u - tile * nkb1, k1 = min(nkb1, k0 + u1b - u);
             const int a = tile / p.tiles_i, ti = tile - a * p.tiles_i, e = R->active[a], n = __popc(R->mask[e]);
@@ -624,7 +658,8 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
         }
     } else if (warp >= 4) {  // ------------------------------------- promotion
         const int group = (warp - 4) / 4, r = (warp & 3) * 32 + lane;
-        const bool first_thread = warp == 4 && lane == 0;
+        const int pt = threadIdx.x - 128;  // 0 .. 255
+        const bool first_thread = pt == 0;
         const uint32_t lanes = taddr + ((uint32_t)(warp & 3) << 21);
         uint32_t it = 0;
         // Once a wait has given up, the warps stop waiting but keep step (they
@@ -651,15 +686,15 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
         // Adds `len` of a tile's `whole` units to its counter once the pieces
         // of all 256 threads are written; true for the CTA that completes it.
         const auto is_last = [&](int* counter, int len, int whole) {
-            __threadfence();
             bar_promotion();
-            if (first_thread) {
+            if (first_thread) {  // its fence covers what the barrier has ordered before it
+                __threadfence();
                 const int old = atomicAdd(counter, len);
                 S->last = old + len == whole;
                 if (S->last) *counter = 0;  // for the next call
+                __threadfence();
             }
             bar_promotion();
-            if (S->last) __threadfence();
             return S->last != 0;
         };
 
@@ -688,8 +723,12 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
                 float* dst = p.part1 + ((int64_t)(blockIdx.x * 2 + (k0 > 0 ? 0 : 1)) * p.tokens) * 256 + group * 128 + r;
 #pragma unroll 2
                 for (int i = 0; i < n; ++i) __stcg(dst + i * 256, own[i * 256]);
-                if ((mine = is_last(p.cnt1 + tile, len, nkb1)))
-                    join(own, 256, n, p.part1 + group * 128 + r, (int64_t)p.tokens * 256, total1, tile * nkb1, nkb1);
+                if ((mine = is_last(p.cnt1 + tile, len, nkb1))) {
+                    const int first = tile * nkb1, c0 = owner(total1, first), c1 = owner(total1, first + nkb1 - 1);
+                    for (int i = pt * 4; i < n * 256; i += 1024)
+                        *reinterpret_cast<float4*>(sums + i) =
+                            join4(p.part1, (int64_t)p.tokens * 256, i, S->cuts[0], c0, c1, first);
+                }
             }
             if (mine) {  // h = silu(gate) * up, and its digits; group g takes the tokens of its parity
                 bar_promotion();
@@ -716,7 +755,6 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
             bar_promotion();  // `sums` is read
             u += len;
         }
-        __threadfence();
         fence_proxy_all();  // the digits are read by TMA
         bar_promotion();
         if (first_thread) {
@@ -754,28 +792,29 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
                 v += run;
             }
             bar_promotion();
-            // the two groups' sums meet; group g finishes the tokens of its parity
-            float* both = sums + r;
-#pragma unroll 2
-            for (int i = group; i < p.tokens; i += 2) both[i * 128] += both[(p.tokens + i) * 128];
-            bool mine = len == per;
-            if (!mine) {
-                float* dst = p.part2 + ((int64_t)(blockIdx.x * 2 + (k0 > 0 ? 0 : 1)) * p.tokens) * 128 + r;
-#pragma unroll 2
-                for (int i = group; i < p.tokens; i += 2) __stcg(dst + i * 128, both[i * 128]);
-                if ((mine = is_last(p.cnt2 + rt, len, per)))
-                    join(both + group * 128, 256, (p.tokens - group + 1) / 2, p.part2 + group * 128 + r,
-                         (int64_t)p.tokens * 128, total2, rt * per, per);
+            // the two groups' sums meet; a thread takes four rows of a token
+            const bool whole = len == per;
+            float* dst = p.part2 + ((int64_t)(blockIdx.x * 2 + (k0 > 0 ? 0 : 1)) * p.tokens) * 128;
+            for (int i = pt * 4; i < p.tokens * 128; i += 1024) {
+                float4 v = *reinterpret_cast<const float4*>(sums + i);
+                const float4 w = *reinterpret_cast<const float4*>(sums + p.tokens * 128 + i);
+                v.x += w.x, v.y += w.y, v.z += w.z, v.w += w.w;
+                if (whole)
+                    store_y(p, i / 128, rt * 128 + i % 128, v);
+                else
+                    __stcg(reinterpret_cast<float4*>(dst + i), v);
             }
-            if (mine && rt * 128 + r < p.hidden) {
-#pragma unroll 1
-                for (int i = group; i < p.tokens; i += 2)
-                    store_out(p.y, i * p.ldy + rt * 128 + r, p.bf16 ? kBF16 : kF16, both[i * 128]);
+            if (!whole && is_last(p.cnt2 + rt, len, per)) {
+                const int first = rt * per, c0 = owner(total2, first), c1 = owner(total2, first + per - 1);
+                for (int i = pt * 4; i < p.tokens * 128; i += 1024)
+                    store_y(p, i / 128, rt * 128 + i % 128,
+                            join4(p.part2, (int64_t)p.tokens * 128, i, S->cuts[1], c0, c1, first));
             }
             bar_promotion();  // `sums` is read
             u += len;
         }
     }
+    __syncwarp();  // one lane ran the role: the barrier counts whole warps
     __syncthreads();
     tc_fence_after();
     if (warp == 1) tmem_dealloc(taddr, 512);

@@ -89,7 +89,7 @@ extern "C" SQZ_API sqz_status sqz_create_moe(const sqz_moe_desc* desc, sqz_moe_t
     if (!m) return host_fail(SQZ_ERR_OOM, "no host memory for the handle");
     m->d = d;
     m->device = dev.device;
-    m->sms = dev.sms;
+    m->sms = dev.sms < M::kMaxGrid ? dev.sms : M::kMaxGrid;
     m->smem = dev.smem;
     m->tiles_i = (int)tiles_i;
     m->tiles_h = (int)tiles_h;
@@ -184,7 +184,7 @@ extern "C" SQZ_API sqz_status sqz_moe_forward(sqz_moe_t moe, const void* x, int3
     p.vec = reinterpret_cast<uintptr_t>(x) % 16 == 0 && ldx % 8 == 0 && reinterpret_cast<uintptr_t>(d.router) % 16 == 0 &&
             d.ld_router % 8 == 0;
     p.stage_bytes = 16384 + M::b_rows(tokens) * 128;
-    const int fixed = kSharedSlack + 2 * tokens * 128 * 4 + (int)sizeof(M::Shared);
+    const int fixed = kSharedSlack + 2 * tokens * 128 * 4 + M::scratch_bytes(tokens, d.experts) + (int)sizeof(M::Shared);
     p.stages = (moe->smem - fixed) / p.stage_bytes;
     if (p.stages > M::kMaxRing) p.stages = M::kMaxRing;
     CUtensorMap mx, mh;
