@@ -326,8 +326,8 @@ __device__ __forceinline__ void route_token(const Params& p, Routing* R, uint32_
     }
 }
 
-// Active experts in ascending order, the first row of each, and the rows'
-// tokens and weights (one warp).
+// Active experts in ascending order, the first row of each (one
+// warp).
 __device__ __forceinline__ void list_experts(const Params& p, Routing* R, int lane) {
     int n = 0, rows = 0, most = 0;
     for (int e0 = 0; e0 < p.experts; e0 += 32) {
@@ -351,46 +351,56 @@ __device__ __forceinline__ void list_experts(const Params& p, Routing* R, int la
     }
     most = __reduce_max_sync(0xffffffffu, most);
     if (lane == 0) R->n_active = n, R->n_most = most;
-    __syncwarp();
-    for (int i = lane; i < p.tokens * p.top_k; i += 32) {
-        const int t = i / p.top_k, e = R->id[i];
-        const int row = R->base[e] + __popc(R->mask[e] & ((1u << t) - 1));
-        R->row_token[row] = (uint8_t)t;
-        R->row_weight[row] = R->weight[i];
-    }
 }
 
 // -------------------------------------------------------- unit sequences
-// `total` units cut evenly: CTA c has [cuts[c], cuts[c + 1]).  The table is in
-// shared memory (a 64-bit division each, once).
+// `total` units cut evenly: CTA c has [cuts[c], cuts[c + 1]), cuts[c] =
+// floor(total c / grid) (in 32 bits: the remainder times c stays below grid^2).
 __device__ __forceinline__ void make_cuts(int* cuts, int total) {
-    for (int c = threadIdx.x; c <= gridDim.x; c += kThreads) cuts[c] = (int)((int64_t)total * c / gridDim.x);
+    const int g = gridDim.x, q = total / g, r = total - q * g;
+    for (int c = threadIdx.x; c <= g; c += kThreads) cuts[c] = q * c + r * c / g;
 }
-// The CTA that has unit u.
-__device__ __forceinline__ int owner(int total, int u) {
-    return (int)((((int64_t)u + 1) * gridDim.x - 1) / total);
+// The last CTA that starts at or before unit u: the one that has it.
+__device__ __forceinline__ int owner(const int* cuts, int u) {
+    int lo = 0, hi = gridDim.x;  // cuts[lo] <= u < cuts[hi]
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (cuts[mid] <= u) lo = mid; else hi = mid;
+    }
+    return lo;
 }
 
-// Four consecutive floats of a tile's sum: its pieces added in CTA order.
-// Pieces lie [CTA][at the tile's start: 1, later: 0][size floats]; `at` is the
-// place in a piece.  All the loads of a group of eight pieces are in flight
-// together.
-__device__ __forceinline__ float4 join4(const float* pieces, int64_t size, int at, const int* cuts, int c0, int c1,
-                                        int first) {
-    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+// Sums of a tile's pieces in CTA order: four consecutive floats at `at` and
+// four more 1024 floats further on (256 threads cover a run of 1024).  Pieces
+// lie [CTA][at the tile's start: 1, later: 0][size floats], `size` of them in
+// use.  The loads of up to eight pieces are in flight together.
+struct Joined {
+    float4 v[2];
+};
+__device__ __forceinline__ Joined join4(const float* pieces, int64_t size, int at, const int* cuts, int c0, int c1,
+                                        int first, int used) {
+    Joined s;
+    s.v[0] = s.v[1] = make_float4(0.f, 0.f, 0.f, 0.f);
+    const bool two = at + 1024 < used;
     for (int cb = c0; cb <= c1; cb += 8) {
-        float4 w[8];
+        float4 w[2][8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const int c = min(cb + j, c1), from = cuts[c];
-            w[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (cb + j <= c1 && from < cuts[c + 1])
-                w[j] = __ldcg(reinterpret_cast<const float4*>(pieces + (c * 2 + (from > first ? 0 : 1)) * size + at));
+            const bool on = cb + j <= c1 && from < cuts[c + 1];
+            const float4* src =
+                reinterpret_cast<const float4*>(pieces + (c * 2 + (from > first ? 0 : 1)) * size + at);
+            w[0][j] = w[1][j] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (on) w[0][j] = __ldcg(src);
+            if (on && two) w[1][j] = __ldcg(src + 256);
         }
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v.x += w[j].x, v.y += w[j].y, v.z += w[j].z, v.w += w[j].w;
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                s.v[k].x += w[k][j].x, s.v[k].y += w[k][j].y, s.v[k].z += w[k][j].z, s.v[k].w += w[k][j].w;
     }
-    return v;
+    return s;
 }
 
 // Four consecutive columns of y (hidden is a multiple of 16: all or none).
@@ -514,6 +524,12 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
     uint32_t bufs = kMaxBufs, bufs_log = 3;
     while (bufs * 2 * cols > 512) bufs /= 2, --bufs_log;
     const int total1 = n_act * p.tiles_i * nkb1, total2 = p.tiles_h * n_act * nkb2;
+    for (int i = threadIdx.x; i < (*dead ? 0 : p.tokens * p.top_k); i += kThreads) {
+        const int t = i / p.top_k, e = R->id[i];
+        const int row = R->base[e] + __popc(R->mask[e] & ((1u << t) - 1));
+        R->row_token[row] = (uint8_t)t;
+        R->row_weight[row] = R->weight[i];
+    }
     make_cuts(S->cuts[0], total1);
     make_cuts(S->cuts[1], total2);
     __syncthreads();
@@ -724,10 +740,14 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
 #pragma unroll 2
                 for (int i = 0; i < n; ++i) __stcg(dst + i * 256, own[i * 256]);
                 if ((mine = is_last(p.cnt1 + tile, len, nkb1))) {
-                    const int first = tile * nkb1, c0 = owner(total1, first), c1 = owner(total1, first + nkb1 - 1);
-                    for (int i = pt * 4; i < n * 256; i += 1024)
-                        *reinterpret_cast<float4*>(sums + i) =
-                            join4(p.part1, (int64_t)p.tokens * 256, i, S->cuts[0], c0, c1, first);
+                    const int first = tile * nkb1, c0 = owner(S->cuts[0], first);
+                    const int c1 = owner(S->cuts[0], first + nkb1 - 1);
+                    for (int i = pt * 4; i < n * 256; i += 2048) {
+                        const Joined s =
+                            join4(p.part1, (int64_t)p.tokens * 256, i, S->cuts[0], c0, c1, first, n * 256);
+                        *reinterpret_cast<float4*>(sums + i) = s.v[0];
+                        if (i + 1024 < n * 256) *reinterpret_cast<float4*>(sums + i + 1024) = s.v[1];
+                    }
                 }
             }
             if (mine) {  // h = silu(gate) * up, and its digits; group g takes the tokens of its parity
@@ -805,10 +825,13 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
                     __stcg(reinterpret_cast<float4*>(dst + i), v);
             }
             if (!whole && is_last(p.cnt2 + rt, len, per)) {
-                const int first = rt * per, c0 = owner(total2, first), c1 = owner(total2, first + per - 1);
-                for (int i = pt * 4; i < p.tokens * 128; i += 1024)
-                    store_y(p, i / 128, rt * 128 + i % 128,
-                            join4(p.part2, (int64_t)p.tokens * 128, i, S->cuts[1], c0, c1, first));
+                const int first = rt * per, used = p.tokens * 128, c0 = owner(S->cuts[1], first);
+                const int c1 = owner(S->cuts[1], first + per - 1);
+                for (int i = pt * 4; i < used; i += 2048) {
+                    const Joined s = join4(p.part2, used, i, S->cuts[1], c0, c1, first, used);
+                    store_y(p, i / 128, rt * 128 + i % 128, s.v[0]);
+                    if (i + 1024 < used) store_y(p, i / 128 + 8, rt * 128 + i % 128, s.v[1]);
+                }
             }
             bar_promotion();  // `sums` is read
             u += len;
