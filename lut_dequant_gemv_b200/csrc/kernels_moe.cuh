@@ -97,7 +97,7 @@ struct Params {
     int tokens, experts, top_k, hidden, inter;
     int tiles_i, tiles_h;  // also the blocks of K of the down and the gate/up products
     int hpad, ipad;
-    int bf16, renormalize, vec;
+    int renormalize, vec;
     int stages, stage_bytes;
 };
 
@@ -109,9 +109,10 @@ __host__ __device__ inline int scratch_bytes(int tokens, int experts) {
     return ((keys > share ? keys : share) + 127) / 128 * 128;
 }
 
-__device__ __forceinline__ float load_x(const uint16_t* p, bool bf16) {
+template <bool BF16>
+__device__ __forceinline__ float load_x(const uint16_t* p) {
     const uint16_t h = __ldg(p);
-    return bf16 ? __uint_as_float((uint32_t)h << 16) : __half2float(__ushort_as_half(h));
+    return BF16 ? __uint_as_float((uint32_t)h << 16) : __half2float(__ushort_as_half(h));
 }
 
 // ---------------------------------------------------------- grid barrier
@@ -171,22 +172,24 @@ __device__ __forceinline__ uint32_t digits_of(float v) {
 }
 
 // ------------------------------------------------------------ phase 0
-__device__ __forceinline__ void unpack8(const uint4& u, bool bf16, float (&v)[8]) {
+template <bool BF16>
+__device__ __forceinline__ void unpack8(const uint4& u, float (&v)[8]) {
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        v[2 * j] = bf16 ? __uint_as_float(w[j] << 16) : h2f((uint16_t)w[j]);
-        v[2 * j + 1] = bf16 ? __uint_as_float(w[j] & 0xFFFF0000u) : h2f((uint16_t)(w[j] >> 16));
+        v[2 * j] = BF16 ? __uint_as_float(w[j] << 16) : h2f((uint16_t)w[j]);
+        v[2 * j + 1] = BF16 ? __uint_as_float(w[j] & 0xFFFF0000u) : h2f((uint16_t)(w[j] >> 16));
     }
 }
 // Eight values from column c (zeros past `hidden`; a vector load when rows are
 // 16-byte aligned).
+template <bool BF16>
 __device__ __forceinline__ void load_x8(const uint16_t* row, int c, const Params& p, float (&v)[8]) {
     if (p.vec) {
-        unpack8(c < p.hidden ? ldg_u128(row + c) : make_uint4(0, 0, 0, 0), p.bf16, v);
+        unpack8<BF16>(c < p.hidden ? ldg_u128(row + c) : make_uint4(0, 0, 0, 0), v);
     } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = c + j < p.hidden ? load_x(row + c + j, p.bf16) : 0.f;
+        for (int j = 0; j < 8; ++j) v[j] = c + j < p.hidden ? load_x<BF16>(row + c + j) : 0.f;
     }
 }
 
@@ -195,6 +198,7 @@ __device__ __forceinline__ void load_x8(const uint16_t* row, int c, const Params
 // t's.
 // The expert's row is held in registers (two runs at a time), so a token costs
 // its own loads only; four tokens' sums cross the lanes together.
+template <bool BF16>
 __device__ __forceinline__ float logits_share(const Params& p, int e, int t_begin, int t_end, int warp,
                                               int lane) {
     const uint16_t* r = p.router + (int64_t)e * p.ld_router;
@@ -202,8 +206,8 @@ __device__ __forceinline__ float logits_share(const Params& p, int e, int t_begi
     for (int c0 = warp * 256; c0 < p.hidden; c0 += 2 * kWarps * 256) {
         const int ca = c0 + lane * 8, cb = ca + kWarps * 256;
         float ra[8], rb[8];
-        load_x8(r, ca, p, ra);
-        load_x8(r, cb, p, rb);
+        load_x8<BF16>(r, ca, p, ra);
+        load_x8<BF16>(r, cb, p, rb);
 #pragma unroll 2
         for (int t0 = t_begin; t0 < t_end; t0 += 4) {
             float s[4];
@@ -211,8 +215,8 @@ __device__ __forceinline__ float logits_share(const Params& p, int e, int t_begi
             for (int i = 0; i < 4; ++i) {
                 const uint16_t* x = p.x + (int64_t)min(t0 + i, t_end - 1) * p.ldx;
                 float xa[8], xb[8];
-                load_x8(x, ca, p, xa);
-                load_x8(x, cb, p, xb);
+                load_x8<BF16>(x, ca, p, xa);
+                load_x8<BF16>(x, cb, p, xb);
                 s[i] = 0.f;
 #pragma unroll
                 for (int j = 0; j < 8; ++j) s[i] = fmaf(ra[j], xa[j], fmaf(rb[j], xb[j], s[i]));
@@ -234,13 +238,14 @@ __device__ __forceinline__ float logits_share(const Params& p, int e, int t_begi
 }
 
 // Digits of block kb of token t: lane holds four consecutive values.
+template <bool BF16>
 __device__ __forceinline__ void x_digits_unit(const Params& p, int t, int kb, int lane) {
     float v[4];
     uint32_t m = 0;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         const int c = kb * kBlockK + lane * 4 + j;
-        v[j] = c < p.hidden ? load_x(p.x + (int64_t)t * p.ldx + c, p.bf16) : 0.f;
+        v[j] = c < p.hidden ? load_x<BF16>(p.x + (int64_t)t * p.ldx + c) : 0.f;
         m = max(m, __float_as_uint(v[j]) & 0x7FFFFFFFu);
     }
     m = __reduce_max_sync(0xffffffffu, m);
@@ -404,10 +409,11 @@ __device__ __forceinline__ Joined join4(const float* pieces, int64_t size, int a
 }
 
 // Four consecutive columns of y (hidden is a multiple of 16: all or none).
+template <bool BF16>
 __device__ __forceinline__ void store_y(const Params& p, int token, int col, const float4& v) {
     if (col >= p.hidden) return;
     const int64_t at = token * p.ldy + col;
-    const int type = p.bf16 ? kBF16 : kF16;
+    const int type = BF16 ? kBF16 : kF16;
     store_out(p.y, at, type, v.x);
     store_out(p.y, at + 1, type, v.y);
     store_out(p.y, at + 2, type, v.z);
@@ -444,6 +450,7 @@ __device__ __forceinline__ void promote4(float (&acc)[4], uint32_t taddr, const 
     }
 }
 
+template <bool BF16>
 __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant__ CUtensorMap map_w13,
                                                           const __grid_constant__ CUtensorMap map_w2,
                                                           const __grid_constant__ CUtensorMap map_x,
@@ -458,6 +465,13 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int nkb1 = p.tiles_h, nkb2 = p.tiles_i;  // blocks of K of the two products
 
+    // an expert's tokens in as many groups (of whole fours) as there are CTAs for
+    int groups = max(1, min((p.tokens + 3) / 4, (int)gridDim.x / p.experts));
+    const int per_group = ((p.tokens + 3) / 4 + groups - 1) / groups * 4;
+    groups = (p.tokens + per_group - 1) / per_group;
+    if (blockIdx.x < p.experts * groups)  // the router's row on its way while x is split
+        for (int c = threadIdx.x * 64; c < p.hidden; c += kThreads * 64)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(p.router + blockIdx.x / groups * p.ld_router + c));
     if (warp == 1) tmem_alloc(&S->taddr, 512);
     if (threadIdx.x == 0) {
         S->dead = 0;
@@ -480,14 +494,10 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
     // ---- phase 0: logits and the digits of x
     float* share = reinterpret_cast<float*>(scratch);  // [kWarps][32]
     for (int u = gridDim.x - 1 - blockIdx.x + gridDim.x * warp; u < p.tokens * nkb1; u += gridDim.x * kWarps)
-        x_digits_unit(p, u / nkb1, u % nkb1, lane);
-    // an expert's tokens in as many groups (of whole fours) as there are CTAs for
-    int groups = max(1, min((p.tokens + 3) / 4, (int)gridDim.x / p.experts));
-    const int per_group = ((p.tokens + 3) / 4 + groups - 1) / groups * 4;
-    groups = (p.tokens + per_group - 1) / per_group;
+        x_digits_unit<BF16>(p, u / nkb1, u % nkb1, lane);
     for (int u = blockIdx.x; u < p.experts * groups; u += gridDim.x) {
         const int e = u / groups, t0 = (u - e * groups) * per_group, t1 = min(t0 + per_group, p.tokens);
-        share[warp * 32 + lane] = logits_share(p, e, t0, t1, warp, lane);
+        share[warp * 32 + lane] = logits_share<BF16>(p, e, t0, t1, warp, lane);
         __syncthreads();
         const int t = t0 + threadIdx.x;
         if (t < t1) {
@@ -820,7 +830,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
                 const float4 w = *reinterpret_cast<const float4*>(sums + p.tokens * 128 + i);
                 v.x += w.x, v.y += w.y, v.z += w.z, v.w += w.w;
                 if (whole)
-                    store_y(p, i / 128, rt * 128 + i % 128, v);
+                    store_y<BF16>(p, i / 128, rt * 128 + i % 128, v);
                 else
                     __stcg(reinterpret_cast<float4*>(dst + i), v);
             }
@@ -829,8 +839,8 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
                 const int c1 = owner(S->cuts[1], first + per - 1);
                 for (int i = pt * 4; i < used; i += 2048) {
                     const Joined s = join4(p.part2, used, i, S->cuts[1], c0, c1, first, used);
-                    store_y(p, i / 128, rt * 128 + i % 128, s.v[0]);
-                    if (i + 1024 < used) store_y(p, i / 128 + 8, rt * 128 + i % 128, s.v[1]);
+                    store_y<BF16>(p, i / 128, rt * 128 + i % 128, s.v[0]);
+                    if (i + 1024 < used) store_y<BF16>(p, i / 128 + 8, rt * 128 + i % 128, s.v[1]);
                 }
             }
             bar_promotion();  // `sums` is read

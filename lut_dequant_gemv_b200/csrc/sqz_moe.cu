@@ -179,7 +179,6 @@ extern "C" SQZ_API sqz_status sqz_moe_forward(sqz_moe_t moe, const void* x, int3
     p.tiles_h = moe->tiles_h;
     p.hpad = moe->tiles_h * 128;
     p.ipad = moe->tiles_i * 128;
-    p.bf16 = d.x_type == SQZ_TYPE_BF16;
     p.renormalize = d.renormalize;
     p.vec = reinterpret_cast<uintptr_t>(x) % 16 == 0 && ldx % 8 == 0 && reinterpret_cast<uintptr_t>(d.router) % 16 == 0 &&
             d.ld_router % 8 == 0;
@@ -191,8 +190,10 @@ extern "C" SQZ_API sqz_status sqz_moe_forward(sqz_moe_t moe, const void* x, int3
     if ((st = tile_map(&mx, p.xq, p.hpad, (int64_t)tokens * M::kDigits, p.hpad, M::kDigits)) != SQZ_OK) return st;
     if ((st = tile_map(&mh, p.hq, p.ipad, (int64_t)tokens * d.top_k * M::kDigits, p.ipad, M::kDigits)) != SQZ_OK)
         return st;
-    static std::atomic<uint64_t> ready;
-    if ((st = allow_smem(M::moe_kernel, dev, &ready)) != SQZ_OK) return st;
+    const bool bf16 = d.x_type == SQZ_TYPE_BF16;
+    const auto kernel = bf16 ? M::moe_kernel<true> : M::moe_kernel<false>;
+    static std::atomic<uint64_t> ready[2];
+    if ((st = allow_smem(kernel, dev, &ready[bf16])) != SQZ_OK) return st;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)moe->sms);
     cfg.blockDim = dim3(M::kThreads);
@@ -203,7 +204,7 @@ extern "C" SQZ_API sqz_status sqz_moe_forward(sqz_moe_t moe, const void* x, int3
     attr[0].val.cooperative = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    SQZ_F8_TRY(cudaLaunchKernelEx(&cfg, M::moe_kernel, moe->map_w13, moe->map_w2, mx, mh, p), "moe launch");
+    SQZ_F8_TRY(cudaLaunchKernelEx(&cfg, kernel, moe->map_w13, moe->map_w2, mx, mh, p), "moe launch");
     return SQZ_OK;
 }
 
