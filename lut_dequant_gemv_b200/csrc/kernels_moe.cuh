@@ -121,13 +121,16 @@ __device__ __forceinline__ unsigned long long ld_acquire(const unsigned long lon
     asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(p) : "memory");
     return v;
 }
+// Release and acquire at GPU scope (__threadfence is sequentially consistent,
+// which nothing here needs, and slower).
+__device__ __forceinline__ void fence_gpu() { asm volatile("fence.acq_rel.gpu;" ::: "memory"); }
 __device__ __forceinline__ void fence_proxy_all() { asm volatile("fence.proxy.async;" ::: "memory"); }
 
 // One thread of a CTA arrives, and later waits for the round its arrival
 // belongs to.  The grid is launched cooperatively (every CTA is resident), and
 // the wait is bounded all the same (about four seconds).
 __device__ __forceinline__ unsigned long long grid_arrive(Header* h) {
-    __threadfence();
+    fence_gpu();
     const unsigned long long old = atomicAdd(&h->arrived, 1ull);
     return (old / gridDim.x + 1) * gridDim.x;
 }
@@ -139,7 +142,7 @@ __device__ __forceinline__ bool grid_wait(const Header* h, unsigned long long ta
             return false;
         }
     }
-    __threadfence();
+    fence_gpu();
     return true;
 }
 
@@ -714,11 +717,11 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
         const auto is_last = [&](int* counter, int len, int whole) {
             bar_promotion();
             if (first_thread) {  // its fence covers what the barrier has ordered before it
-                __threadfence();
+                fence_gpu();
                 const int old = atomicAdd(counter, len);
                 S->last = old + len == whole;
                 if (S->last) *counter = 0;  // for the next call
-                __threadfence();
+                fence_gpu();
             }
             bar_promotion();
             return S->last != 0;
