@@ -24,14 +24,14 @@ namespace f8 {
 // they round to code 0 either way.
 struct Quotient {
     float scale, inv;
-    bool plain;
-    __device__ __forceinline__ explicit Quotient(float s) : scale(s), inv(1.f / s) {
-        plain = !(s >= 0x1p-100f && s <= 0x1p120f);
-    }
-    __device__ __forceinline__ float operator()(float x) const {
-        if (plain) return x / scale;
-        const float q = x * inv;
-        return fmaf(-fmaf(q, scale, -x), inv, q);  // the remainder's sign keeps -0 / scale = -0
+    __device__ __forceinline__ explicit Quotient(float s) : scale(s), inv(1.f / s) {}
+    __device__ __forceinline__ bool divides() const { return !(scale >= 0x1p-100f && scale <= 0x1p120f); }
+    // Two quotients at once (packed fp32 instructions).  The remainder's sign
+    // is such that -0 / scale stays -0.
+    __device__ __forceinline__ void operator()(float& a, float& b) const {
+        const uint64_t x = pack2(-a, -b), ny = pack2(-inv, -inv);
+        const uint64_t q = mul2(x, ny), r = fma2_of(q, pack2(scale, scale), x);
+        unpack2(fma2_of(r, ny, q), a, b);
     }
 };
 
@@ -51,50 +51,92 @@ __device__ __forceinline__ float x_to_float(uint32_t h) {
     return __half2float(__ushort_as_half((uint16_t)h));
 }
 
-// Eight consecutive elements of row `r` from column c (zeros past the edge).
-template <bool BF16, bool VEC>
-__device__ __forceinline__ void load8(const uint16_t* __restrict__ row, int c, int cols, float (&v)[8]) {
-    if (VEC && c + 8 <= cols) {
-        const uint4 u = ldg_stream_u128(row + c);
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+// Eight consecutive elements of a row from column c, as they are stored
+// (zeros past the edge).  ALIGN: the alignment in bytes that x and its pitch
+// have, so the width of the loads.
+struct Raw8 {
+    uint32_t w[4];
+};
+template <int ALIGN>
+__device__ __forceinline__ Raw8 load8(const uint16_t* __restrict__ row, int c, int cols) {
+    Raw8 v;
+    if (ALIGN > 2 && c + 8 <= cols) {
+        const char* p = reinterpret_cast<const char*>(row + c);
+        if (ALIGN == 16) {
+            const uint4 u = ldg_stream_u128(p);
+            v.w[0] = u.x, v.w[1] = u.y, v.w[2] = u.z, v.w[3] = u.w;
+        } else if (ALIGN == 8) {
 #pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const uint2 u = __ldg(reinterpret_cast<const uint2*>(p) + i);
+                v.w[2 * i] = u.x, v.w[2 * i + 1] = u.y;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v.w[i] = __ldg(reinterpret_cast<const uint32_t*>(p) + i);
+        }
+    } else {
+        uint16_t h[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) h[i] = c + i < cols ? __ldg(row + c + i) : 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v.w[i] = h[2 * i] | (uint32_t)h[2 * i + 1] << 16;
+    }
+    return v;
+}
+// The largest magnitude's bits of eight elements, two at a time (16-bit bit
+// patterns order as their values do).
+__device__ __forceinline__ uint32_t max_bits8(const Raw8& v, uint32_t m) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m = __vmaxu2(m, v.w[i] & 0x7FFF7FFFu);
+    return m;
+}
+template <bool BF16>
+__device__ __forceinline__ uint32_t fp32_bits(uint32_t m) {
+    return __float_as_uint(x_to_float<BF16>(max(m & 0xFFFFu, m >> 16)));
+}
+
+template <bool BF16, bool E5M2>
+__device__ __forceinline__ uint2 codes8(const Raw8& raw, const Quotient& by) {
+    uint32_t w[4];
+    if (by.divides()) {  // one test a block, and a loop: rare
+#pragma unroll 1
         for (int i = 0; i < 4; ++i) {
-            v[2 * i] = x_to_float<BF16>(w[i] & 0xFFFF);
-            v[2 * i + 1] = x_to_float<BF16>(w[i] >> 16);
+            const uint32_t h = i == 0 ? raw.w[0] : i == 1 ? raw.w[1] : i == 2 ? raw.w[2] : raw.w[3];
+            const uint32_t c2 = code2<E5M2>(x_to_float<BF16>(h & 0xFFFF) / by.scale, x_to_float<BF16>(h >> 16) / by.scale);
+            if (i == 0) w[0] = c2;
+            if (i == 1) w[1] = c2;
+            if (i == 2) w[2] = c2;
+            if (i == 3) w[3] = c2;
         }
     } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = c + i < cols ? x_to_float<BF16>(__ldg(row + c + i)) : 0.f;
+        for (int i = 0; i < 4; ++i) {
+            float a = x_to_float<BF16>(raw.w[i] & 0xFFFF), b = x_to_float<BF16>(raw.w[i] >> 16);
+            by(a, b);
+            w[i] = code2<E5M2>(a, b);
+        }
     }
+    return make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
 }
-
-template <bool E5M2>
-__device__ __forceinline__ void store8(uint8_t* __restrict__ row, int c, int cols, const float (&v)[8],
-                                       const Quotient& by) {
-    uint32_t lo = 0, hi = 0;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        lo |= code2<E5M2>(by(v[2 * i]), by(v[2 * i + 1])) << (16 * i);
-        hi |= code2<E5M2>(by(v[4 + 2 * i]), by(v[4 + 2 * i + 1])) << (16 * i);
-    }
+// Eight codes to columns c .. of a row (rows are 16-byte aligned).
+__device__ __forceinline__ void store_codes(uint8_t* __restrict__ row, int c, int cols, const uint2& q) {
     if (c + 8 <= cols) {
-        *reinterpret_cast<uint2*>(row + c) = make_uint2(lo, hi);  // rows are 16-byte aligned
+        *reinterpret_cast<uint2*>(row + c) = q;
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            if (c + i < cols) row[c + i] = (uint8_t)((i < 4 ? lo >> (8 * i) : hi >> (8 * (i - 4))) & 0xFF);
+            if (c + i < cols) row[c + i] = (uint8_t)((i < 4 ? q.x >> (8 * i) : q.y >> (8 * (i - 4))) & 0xFF);
     }
-}
-
-__device__ __forceinline__ uint32_t max_bits8(const float (&v)[8], uint32_t m) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
-    return m;
 }
 
 template <bool E5M2>
 __device__ __forceinline__ float scale_of(uint32_t max_bits) {
-    return max_bits ? __uint_as_float(max_bits) / (E5M2 ? 57344.f : 448.f) : 1.f;
+    if (max_bits == 0) return 1.f;
+    const float m = __uint_as_float(max_bits), f = E5M2 ? 57344.f : 448.f, inv = 1.f / f;  // (a constant)
+    if (!(m >= 0x1p-90f && m <= 0x1p126f)) return m / f;
+    const float q = m * inv;
+    return fmaf(fmaf(-q, f, m), inv, q);  // correctly rounded, as above
 }
 
 struct QuantParams {
@@ -108,39 +150,69 @@ struct QuantParams {
     int rows, cols, nblocks;  // nblocks = scale blocks of a row
 };
 
-// Blocks of 1 x 128: 16 lanes hold a block, 8 elements each; a warp takes two
-// blocks a step and strides over all rows x blocks.
-template <bool BF16, bool E5M2, bool VEC>
+// Blocks of 1 x 128: 8 lanes hold a block, 16 elements each (two loads), so
+// that the block's own work (two divisions, the maximum's shuffles, addresses)
+// is spread over more elements -- the kernel is bound by its instructions --
+// and have kAhead blocks in flight: one where the blocks do not fill the SMs (a
+// token), else two.  A warp takes 4 kAhead consecutive blocks a step and strides
+// over all rows x blocks.
+template <bool BF16, bool E5M2, int ALIGN, int kAhead>
 __global__ void __launch_bounds__(256) fp8_quantize_rows_kernel(const QuantParams p) {
     pdl_launch_dependents();
     pdl_wait_previous();
-    const int lane16 = threadIdx.x & 15;
+    const int part = (threadIdx.x & 7) * 16;  // of the block
     const int64_t total = p.batch * p.rows * p.nblocks;
     const bool narrow = total <= 0x7fffffff;  // 32-bit division (the 64-bit one costs as much as a block)
-    const int64_t step = (int64_t)gridDim.x * (blockDim.x / 16);
+    const int64_t step = (int64_t)gridDim.x * (blockDim.x / 8) * kAhead;
     // the loop's bound is the same for the whole warp: its shuffles need every lane
-    for (int64_t first = (int64_t)blockIdx.x * (blockDim.x / 16) + (threadIdx.x / 32) * 2; first < total;
+    for (int64_t first = ((int64_t)blockIdx.x * (blockDim.x / 32) + threadIdx.x / 32) * 4 * kAhead; first < total;
          first += step) {
-        const int64_t at = first + ((threadIdx.x >> 4) & 1);
-        const bool live = at < total;
-        const int64_t row = !live ? 0 : narrow ? (int64_t)((uint32_t)at / (uint32_t)p.nblocks) : at / p.nblocks;
-        const int b = live ? (int)(at - row * p.nblocks) : 0;
-        const int c = b * kBlockK + lane16 * 8;
-        float v[8];
-        load8<BF16, VEC>(p.x + row * p.ldx, c, p.cols, v);
-        uint32_t m = max_bits8(v, 0);
+        Raw8 v[kAhead][2];
+        int64_t row[kAhead];
+        int b[kAhead];
+        const int64_t at = first + ((threadIdx.x >> 3) & 3);
+        row[0] = narrow ? (int64_t)((uint32_t)at / (uint32_t)p.nblocks) : at / p.nblocks;
+        b[0] = (int)(at - row[0] * p.nblocks);
 #pragma unroll
-        for (int off = 8; off > 0; off >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, off));
-        const float s = scale_of<E5M2>(m);
-        if (!live) continue;
-        if (c < p.cols) store8<E5M2>(p.q + row * p.ldq, c, p.cols, v, Quotient(s));
-        if (lane16 == 0) p.scale[row * p.lds + b] = s;
+        for (int i = 0; i < kAhead; ++i) {
+            if (i > 0) {
+                row[i] = row[i - 1], b[i] = b[i - 1] + 4;
+                while (b[i] >= p.nblocks) b[i] -= p.nblocks, ++row[i];
+            }
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                if (at + 4 * i < total)
+                    v[i][k] = load8<ALIGN>(p.x + row[i] * p.ldx, b[i] * kBlockK + part + 8 * k, p.cols);
+                else
+                    v[i][k].w[0] = v[i][k].w[1] = v[i][k].w[2] = v[i][k].w[3] = 0;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            uint32_t m = max_bits8(v[i][1], max_bits8(v[i][0], 0));
+#pragma unroll
+            for (int off = 4; off > 0; off >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, off));
+            const float s = scale_of<E5M2>(fp32_bits<BF16>(m));
+            if (at + 4 * i >= total) continue;
+            const int c = b[i] * kBlockK + part;
+            const Quotient by(s);
+            uint8_t* q = p.q + row[i] * p.ldq;
+            const uint2 lo = codes8<BF16, E5M2>(v[i][0], by), hi = codes8<BF16, E5M2>(v[i][1], by);
+            if (c + 16 <= p.cols) {
+                *reinterpret_cast<uint4*>(q + c) = make_uint4(lo.x, lo.y, hi.x, hi.y);
+            } else {
+                store_codes(q, c, p.cols, lo);
+                store_codes(q, c + 8, p.cols, hi);
+            }
+            if (part == 0) p.scale[row[i] * p.lds + b[i]] = s;
+        }
     }
 }
 
 // Blocks of 128 x 128: one CTA per block, the block in registers (64 elements
-// a thread) between the maximum and the division, so x is read once.
-template <bool BF16, bool E5M2, bool VEC>
+// a thread, all its loads in flight) between the maximum and the division, so
+// x is read once.
+template <bool BF16, bool E5M2, int ALIGN>
 __global__ void __launch_bounds__(256) fp8_quantize_tiles_kernel(const QuantParams p) {
     pdl_launch_dependents();
     pdl_wait_previous();
@@ -151,32 +223,30 @@ __global__ void __launch_bounds__(256) fp8_quantize_tiles_kernel(const QuantPara
     const int r0 = rb * 128 + (threadIdx.x >> 4), c = b * kBlockK + (threadIdx.x & 15) * 8;
     const uint16_t* x = p.x + z * p.rows * p.ldx;
     uint8_t* q = p.q + z * p.rows * p.ldq;
-    float v[8][8];
+    Raw8 v[8];
     uint32_t m = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const int r = r0 + 16 * i;
-        if (r < p.rows) {
-            load8<BF16, VEC>(x + (int64_t)r * p.ldx, c, p.cols, v[i]);
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[i][j] = 0.f;
-        }
+        if (r < p.rows)
+            v[i] = load8<ALIGN>(x + (int64_t)r * p.ldx, c, p.cols);
+        else
+            v[i].w[0] = v[i].w[1] = v[i].w[2] = v[i].w[3] = 0;
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) m = max_bits8(v[i], m);
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, off));
+    for (int off = 16; off > 0; off >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, off));
     if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = m;
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m = max(m, part[i]);
-    const float s = scale_of<E5M2>(m);
+    for (int i = 0; i < 8; ++i) m = __vmaxu2(m, part[i]);
+    const float s = scale_of<E5M2>(fp32_bits<BF16>(m));
     const Quotient by(s);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const int r = r0 + 16 * i;
-        if (r < p.rows && c < p.cols) store8<E5M2>(q + (int64_t)r * p.ldq, c, p.cols, v[i], by);
+        if (r < p.rows && c < p.cols) store_codes(q + (int64_t)r * p.ldq, c, p.cols, codes8<BF16, E5M2>(v[i], by));
     }
     if (threadIdx.x == 0) p.scale[(z * row_blocks + rb) * p.lds + b] = s;
 }

@@ -35,15 +35,28 @@ cudaError_t launch(void (*kernel)(const Params), dim3 grid, int threads, const P
     return cudaLaunchKernelEx(&cfg, kernel, prm);
 }
 
-template <bool BF16, bool E5M2, bool VEC>
+template <bool BF16, bool E5M2, int ALIGN>
 cudaError_t launch_quantize(const QuantParams& p, int block_rows, int sms, cudaStream_t s) {
     if (block_rows == 1) {
-        const int64_t warps = (p.batch * p.rows * p.nblocks + 1) / 2, ctas = (warps + 7) / 8;
-        const int64_t most = (int64_t)sms * 8 * 4;  // four rounds of the resident CTAs, then each strides
-        return launch(fp8_quantize_rows_kernel<BF16, E5M2, VEC>, dim3((unsigned)(ctas < most ? ctas : most)), 256, p, s);
+        const int64_t blocks = p.batch * p.rows * p.nblocks;
+        if (blocks <= (int64_t)sms * 32 * 4)
+            return launch(fp8_quantize_rows_kernel<BF16, E5M2, ALIGN, 1>, dim3((unsigned)((blocks + 31) / 32)), 256, p, s);
+        const int64_t ctas = (blocks + 63) / 64, most = (int64_t)sms * 8 * 4;  // then each strides
+        return launch(fp8_quantize_rows_kernel<BF16, E5M2, ALIGN, 2>, dim3((unsigned)(ctas < most ? ctas : most)), 256,
+                      p, s);
     }
-    return launch(fp8_quantize_tiles_kernel<BF16, E5M2, VEC>,
+    return launch(fp8_quantize_tiles_kernel<BF16, E5M2, ALIGN>,
                   dim3((unsigned)p.nblocks, (unsigned)(p.batch * ((p.rows + 127) / 128))), 256, p, s);
+}
+
+template <bool BF16, bool E5M2>
+cudaError_t launch_quantize(const QuantParams& p, int block_rows, int align, int sms, cudaStream_t s) {
+    switch (align) {
+        case 16: return launch_quantize<BF16, E5M2, 16>(p, block_rows, sms, s);
+        case 8: return launch_quantize<BF16, E5M2, 8>(p, block_rows, sms, s);
+        case 4: return launch_quantize<BF16, E5M2, 4>(p, block_rows, sms, s);
+        default: return launch_quantize<BF16, E5M2, 2>(p, block_rows, sms, s);
+    }
 }
 
 // ------------------------------------------------------------ the product
@@ -166,20 +179,14 @@ extern "C" SQZ_API sqz_status sqz_fp8_quantize(const void* x, int32_t x_type, in
     p.rows = rows;
     p.cols = cols;
     p.nblocks = nblocks;
-    const bool vec = reinterpret_cast<uintptr_t>(x) % 16 == 0 && ldx % 8 == 0;
+    int align = 16;  // of every row
+    while (align > 2 && (reinterpret_cast<uintptr_t>(x) % align || ldx * 2 % align)) align /= 2;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    cudaError_t e;
-    const int kind = (x_type == SQZ_TYPE_BF16 ? 4 : 0) | (format == SQZ_FP8_E5M2 ? 2 : 0) | (vec ? 1 : 0);
-    switch (kind) {
-        case 0: e = launch_quantize<false, false, false>(p, block_rows, d.sms, s); break;
-        case 1: e = launch_quantize<false, false, true>(p, block_rows, d.sms, s); break;
-        case 2: e = launch_quantize<false, true, false>(p, block_rows, d.sms, s); break;
-        case 3: e = launch_quantize<false, true, true>(p, block_rows, d.sms, s); break;
-        case 4: e = launch_quantize<true, false, false>(p, block_rows, d.sms, s); break;
-        case 5: e = launch_quantize<true, false, true>(p, block_rows, d.sms, s); break;
-        case 6: e = launch_quantize<true, true, false>(p, block_rows, d.sms, s); break;
-        default: e = launch_quantize<true, true, true>(p, block_rows, d.sms, s); break;
-    }
+    const bool bf16 = x_type == SQZ_TYPE_BF16, e5m2 = format == SQZ_FP8_E5M2;
+    const cudaError_t e = bf16 ? e5m2 ? launch_quantize<true, true>(p, block_rows, align, d.sms, s)
+                                      : launch_quantize<true, false>(p, block_rows, align, d.sms, s)
+                          : e5m2 ? launch_quantize<false, true>(p, block_rows, align, d.sms, s)
+                                 : launch_quantize<false, false>(p, block_rows, align, d.sms, s);
     SQZ_F8_TRY(e, "fp8 quantize launch");
     return SQZ_OK;
 }
