@@ -96,10 +96,11 @@ __device__ __forceinline__ uint32_t fp32_bits(uint32_t m) {
     return __float_as_uint(x_to_float<BF16>(max(m & 0xFFFFu, m >> 16)));
 }
 
+// The codes of eight elements; `divides`: by.divides() (rare: a loop).
 template <bool BF16, bool E5M2>
-__device__ __forceinline__ uint2 codes8(const Raw8& raw, const Quotient& by) {
+__device__ __forceinline__ uint2 codes8(const Raw8& raw, const Quotient& by, bool divides) {
     uint32_t w[4];
-    if (by.divides()) {  // one test a block, and a loop: rare
+    if (divides) {
 #pragma unroll 1
         for (int i = 0; i < 4; ++i) {
             const uint32_t h = i == 0 ? raw.w[0] : i == 1 ? raw.w[1] : i == 2 ? raw.w[2] : raw.w[3];
@@ -197,7 +198,8 @@ __global__ void __launch_bounds__(256) fp8_quantize_rows_kernel(const QuantParam
             const int c = b[i] * kBlockK + part;
             const Quotient by(s);
             uint8_t* q = p.q + row[i] * p.ldq;
-            const uint2 lo = codes8<BF16, E5M2>(v[i][0], by), hi = codes8<BF16, E5M2>(v[i][1], by);
+            const bool divides = by.divides();
+            const uint2 lo = codes8<BF16, E5M2>(v[i][0], by, divides), hi = codes8<BF16, E5M2>(v[i][1], by, divides);
             if (c + 16 <= p.cols) {
                 *reinterpret_cast<uint4*>(q + c) = make_uint4(lo.x, lo.y, hi.x, hi.y);
             } else {
@@ -213,7 +215,7 @@ __global__ void __launch_bounds__(256) fp8_quantize_rows_kernel(const QuantParam
 // a thread, all its loads in flight) between the maximum and the division, so
 // x is read once.
 template <bool BF16, bool E5M2, int ALIGN>
-__global__ void __launch_bounds__(256) fp8_quantize_tiles_kernel(const QuantParams p) {
+__global__ void __launch_bounds__(256, 4) fp8_quantize_tiles_kernel(const QuantParams p) {
     pdl_launch_dependents();
     pdl_wait_previous();
     __shared__ uint32_t part[8];
@@ -243,11 +245,18 @@ __global__ void __launch_bounds__(256) fp8_quantize_tiles_kernel(const QuantPara
     for (int i = 0; i < 8; ++i) m = __vmaxu2(m, part[i]);
     const float s = scale_of<E5M2>(fp32_bits<BF16>(m));
     const Quotient by(s);
+    const auto write = [&](bool divides) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int r = r0 + 16 * i;
-        if (r < p.rows && c < p.cols) store_codes(q + (int64_t)r * p.ldq, c, p.cols, codes8<BF16, E5M2>(v[i], by));
-    }
+        for (int i = 0; i < 8; ++i) {
+            const int r = r0 + 16 * i;
+            if (r < p.rows && c < p.cols)
+                store_codes(q + (int64_t)r * p.ldq, c, p.cols, codes8<BF16, E5M2>(v[i], by, divides));
+        }
+    };
+    if (by.divides())
+        write(true);
+    else
+        write(false);
     if (threadIdx.x == 0) p.scale[(z * row_blocks + rb) * p.lds + b] = s;
 }
 
