@@ -437,30 +437,47 @@ _H16_TYPES = (torch.float16, torch.bfloat16)
 _TYPES = {torch.float16: SQZ_TYPE_F16, torch.bfloat16: SQZ_TYPE_BF16, torch.float32: SQZ_TYPE_F32}
 
 
-def _on_current_device(t: torch.Tensor, name: str) -> None:
-    if not t.is_cuda:
+_current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
+
+
+def _on_current_device(t: torch.Tensor, name: str) -> int:
+    """The tensor's device, which has to be the current one."""
+    dev = t.get_device()
+    if dev < 0:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+    if dev != _current_device():
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{_current_device()}")
+    return dev
+
+
+def _raw_stream(stream, device: int) -> Optional[int]:
+    """As _stream; torch's current stream of the device without making an object of it (these calls take a
+    few microseconds on the GPU)."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device) or None
+    return _stream(stream)
 
 
 def _pitch(t: torch.Tensor, name: str) -> int:
     """Elements from one row to the next of a tensor whose rows are contiguous and, beyond two
-    dimensions, evenly spaced."""
-    if t.dim() < 2:
+    dimensions, evenly spaced; for a single row, its length rounded up to 16."""
+    shape, strides = t.shape, t.stride()
+    if len(shape) < 2:
         raise ValueError(f"{name} must have at least two dimensions")
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
+    if strides[-1] != 1 and shape[-1] > 1:
         raise ValueError(f"{name} must be row-major")
+    if len(shape) == 2:
+        return strides[0] if shape[0] > 1 else (shape[1] + 15) // 16 * 16
     rows, ld = 1, None
-    for d in range(t.dim() - 2, -1, -1):
-        if t.shape[d] != 1:
+    for d in range(len(shape) - 2, -1, -1):
+        if shape[d] != 1:
             if ld is None:
-                ld = t.stride(d) // rows if t.stride(d) % rows == 0 else -1
-            if t.stride(d) != rows * ld:
+                ld = strides[d] // rows if strides[d] % rows == 0 else -1
+            if strides[d] != rows * ld:
                 raise ValueError(f"{name} must have evenly spaced rows")
-        rows *= t.shape[d]
+        rows *= shape[d]
     if ld is None:  # a single row
-        ld = (t.shape[-1] + 15) // 16 * 16
+        ld = (shape[-1] + 15) // 16 * 16
     return ld
 
 
@@ -470,50 +487,49 @@ def sqz_fp8_quantize(x: torch.Tensor, block_rows: int = 1, dtype: torch.dtype = 
     block_rows (1 or 128) x 128; returns (q, scale).  q has x's shape and an fp8 dtype on a 16-byte row pitch;
     scale is [(batch,) ceil(rows / block_rows), ceil(cols / 128)].  Both are allocated unless given (q's dtype
     then names the format)."""
-    if x.dim() not in (2, 3):
+    shape = x.shape
+    if len(shape) not in (2, 3):
         raise ValueError("x must be [rows, cols] or [batch, rows, cols]")
-    _on_current_device(x, "x")
+    dev = _on_current_device(x, "x")
     if x.dtype not in _H16_TYPES:
         raise TypeError(f"x has dtype {x.dtype}, expected fp16 or bf16")
     if block_rows not in (1, 128):
         raise ValueError("block_rows must be 1 or 128")
-    rows, cols = x.shape[-2:]
+    rows, cols = shape[-2], shape[-1]
     if q is None:
         if dtype not in _FP8_FORMATS:
             raise TypeError(f"dtype {dtype} is not an 8-bit floating-point type")
-        q = torch.empty((*x.shape[:-1], (cols + 15) // 16 * 16), dtype=dtype, device=x.device)[..., :cols]
+        q = torch.empty((*shape[:-1], (cols + 15) // 16 * 16), dtype=dtype, device=x.device)[..., :cols]
     else:
         _on_current_device(q, "q")
-        if q.dtype not in _FP8_FORMATS or q.shape != x.shape:
-            raise ValueError(f"q must have shape {tuple(x.shape)} and an fp8 dtype")
-    shape = (*x.shape[:-2], -(-rows // block_rows), -(-cols // 128))
+        if q.dtype not in _FP8_FORMATS or q.shape != shape:
+            raise ValueError(f"q must have shape {tuple(shape)} and an fp8 dtype")
+    s_shape = (*shape[:-2], -(-rows // block_rows), -(-cols // 128))
     if scale is None:
-        scale = torch.empty(shape, dtype=torch.float32, device=x.device)
+        scale = torch.empty(s_shape, dtype=torch.float32, device=x.device)
     else:
         _on_current_device(scale, "scale")
-        if scale.dtype != torch.float32 or tuple(scale.shape) != shape:
-            raise ValueError(f"scale must be fp32 of shape {shape}")
+        if scale.dtype != torch.float32 or scale.shape != s_shape:
+            raise ValueError(f"scale must be fp32 of shape {s_shape}")
     if x.numel():
-        _check(lib().sqz_fp8_quantize(x.data_ptr(), _TYPES[x.dtype], x.shape[0] if x.dim() == 3 else 1, rows, cols,
-                                      _pitch(x, "x"), block_rows, _FP8_FORMATS[q.dtype], q.data_ptr(), _pitch(q, "q"),
-                                      scale.data_ptr(), _scale_pitch(scale), _stream(stream)), "sqz_fp8_quantize")
+        _check((_lib or lib()).sqz_fp8_quantize(
+            x.data_ptr(), _TYPES[x.dtype], shape[0] if len(shape) == 3 else 1, rows, cols, _pitch(x, "x"), block_rows,
+            _FP8_FORMATS[q.dtype], q.data_ptr(), _pitch(q, "q"), scale.data_ptr(), _pitch(scale, "scale"),
+            _raw_stream(stream, dev)), "sqz_fp8_quantize")
     return q, scale
-
-
-def _scale_pitch(t: torch.Tensor) -> int:
-    return max(_pitch(t, "scale"), t.shape[-1])
 
 
 def _fp8_matrix(q: torch.Tensor, scale: torch.Tensor, name: str, block_rows: int) -> sqz_fp8_matrix:
     _on_current_device(q, name)
-    _on_current_device(scale, f"{name}_scale")
+    _on_current_device(scale, name)
     if q.dtype not in _FP8_FORMATS:
         raise TypeError(f"{name} has dtype {q.dtype}, expected float8_e4m3fn or float8_e5m2")
-    if q.dim() != 2 or scale.dtype != torch.float32 or \
-            scale.shape != (-(-q.shape[0] // block_rows), -(-q.shape[1] // 128)):
+    shape = q.shape
+    if len(shape) != 2 or scale.dtype != torch.float32 or \
+            scale.shape != (-(-shape[0] // block_rows), -(-shape[1] // 128)):
         raise ValueError(f"{name} must be [rows, k] with fp32 scales [ceil(rows / {block_rows}), ceil(k / 128)], got "
-                         f"{tuple(q.shape)} and {tuple(scale.shape)}")
-    return sqz_fp8_matrix(q.data_ptr(), _pitch(q, name), scale.data_ptr(), _scale_pitch(scale), _FP8_FORMATS[q.dtype])
+                         f"{tuple(shape)} and {tuple(scale.shape)}")
+    return sqz_fp8_matrix(q.data_ptr(), _pitch(q, name), scale.data_ptr(), _pitch(scale, "scale"), _FP8_FORMATS[q.dtype])
 
 
 def sqz_fp8_gemm(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor, y: torch.Tensor,
@@ -521,15 +537,14 @@ def sqz_fp8_gemm(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor, w_scal
     """y [m, n] (fp16, bf16 or fp32) = A W^T of 8-bit matrices a [m, k] (scales [m, ceil(k/128)]) and w [n, k]
     (scales [ceil(n/128), ceil(k/128)])."""
     A, W = _fp8_matrix(a, a_scale, "a", 1), _fp8_matrix(w, w_scale, "w", 128)
-    (m, k), n = a.shape, w.shape[0]
-    _on_current_device(y, "y")
-    if w.shape[1] != k or y.shape != (m, n):
+    (m, k), (n, kw) = a.shape, w.shape
+    dev = _on_current_device(y, "y")
+    if kw != k or y.shape != (m, n):
         raise ValueError(f"a {tuple(a.shape)}, w {tuple(w.shape)} and y {tuple(y.shape)} do not fit together")
     if y.dtype not in _TYPES:
         raise TypeError(f"y has dtype {y.dtype}, expected fp16, bf16 or fp32")
-    ldy = max(_pitch(y, "y"), n)
-    _check(lib().sqz_fp8_gemm(ctypes.byref(A), ctypes.byref(W), m, n, k, y.data_ptr(), ldy, _TYPES[y.dtype],
-                              _stream(stream)), "sqz_fp8_gemm")
+    _check((_lib or lib()).sqz_fp8_gemm(ctypes.byref(A), ctypes.byref(W), m, n, k, y.data_ptr(), _pitch(y, "y"),
+                                        _TYPES[y.dtype], _raw_stream(stream, dev)), "sqz_fp8_gemm")
 
 
 def sqz_fp8_status(stream=None) -> int:
@@ -618,13 +633,11 @@ def sqz_moe_forward(moe: Moe, x: torch.Tensor, y: torch.Tensor, ids: Optional[to
     workspace: from sqz_moe_workspace, not shared with a call that may overlap."""
     if workspace is None:
         raise ValueError("workspace is required (sqz_moe_workspace)")
+    tokens, hidden = x.shape[0], moe.hidden
     for name, t in (("x", x), ("y", y)):
-        _on_current_device(t, name)
-        if t.dtype != moe.dtype or t.dim() != 2 or t.shape[1] != moe.hidden or (t.stride(1) != 1 and moe.hidden > 1):
-            raise ValueError(f"{name} must be a row-major [tokens, {moe.hidden}] tensor of {moe.dtype}")
-    tokens = x.shape[0]
-    if y.shape[0] != tokens:
-        raise ValueError(f"x has {tokens} rows, y {y.shape[0]}")
+        dev = _on_current_device(t, name)
+        if t.dtype != moe.dtype or t.shape != (tokens, hidden) or t.stride(1) != 1:
+            raise ValueError(f"{name} must be a row-major [{tokens}, {hidden}] tensor of {moe.dtype}")
     for name, t, dt in (("ids", ids, torch.int32), ("weights", weights, torch.float32)):
         if t is not None:
             _on_current_device(t, name)
@@ -634,10 +647,10 @@ def sqz_moe_forward(moe: Moe, x: torch.Tensor, y: torch.Tensor, ids: Optional[to
     if workspace.dtype != torch.uint8 or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous uint8 tensor")
     one = tokens <= 1
-    _check(lib().sqz_moe_forward(moe, x.data_ptr(), tokens, moe.hidden if one else x.stride(0), y.data_ptr(),
-                                 moe.hidden if one else y.stride(0), None if ids is None else ids.data_ptr(),
-                                 None if weights is None else weights.data_ptr(), workspace.data_ptr(),
-                                 workspace.numel(), _stream(stream)), "sqz_moe_forward")
+    _check((_lib or lib()).sqz_moe_forward(
+        moe, x.data_ptr(), tokens, hidden if one else x.stride(0), y.data_ptr(), hidden if one else y.stride(0),
+        None if ids is None else ids.data_ptr(), None if weights is None else weights.data_ptr(), workspace.data_ptr(),
+        workspace.numel(), _raw_stream(stream, dev)), "sqz_moe_forward")
 
 
 def sqz_moe_status(workspace: torch.Tensor, stream=None) -> int:

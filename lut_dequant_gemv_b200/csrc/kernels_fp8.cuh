@@ -279,7 +279,7 @@ struct GemmParams {
     uint32_t idesc;
     int stages;
     int tiles_m, tiles_n;  // many-row kernel
-    int vec_out;           // y rows are 16-byte aligned
+    int out_align;         // alignment of y's rows in bytes: 32, 16 or less
 };
 
 constexpr int kMaxStages = 12;
@@ -463,34 +463,70 @@ __global__ void __launch_bounds__(224) fp8_gemm_few_kernel(const __grid_constant
 
 // Many rows of A: bound by the tensor cores and by the promotion.  Tiles of
 // 128 rows of A x BN rows of W, a persistent CTA per SM.  A thread of the
-// promotion holds one row of A and BN / 2 columns: the block's scale is then
+// promotion holds one row of A and BN / 4 columns: the block's scale is then
 // one number per thread (the row's scale times the scale of the 128 rows of W
 // that its columns lie in), and the multiply-adds go two to an instruction.
-// Two accumulators in tensor memory let the matrix instructions of block b+1
-// run under the promotion of block b.
+// Accumulators in tensor memory take turns (two of 256 columns), so that the
+// matrix instructions of block b + 1 run under the promotion of block b; with
+// sixteen warps the promotion's loads from tensor memory overlap each other
+// (eight warps of 16-column loads took 1170 cycles a block, where the matrix
+// instructions take 512).
 //
-//   warp 0: TMA ring, warp 1: TMEM and matrix instructions, warps 2-9:
-//   promotion (warp % 4 = the 32 lanes it may read; first or second half of
-//   the columns)
+//   warp 0: TMA ring, warp 1: TMEM and matrix instructions, warps 2-17:
+//   promotion (warp % 4 = the 32 lanes it may read; a quarter of the columns)
 template <int BN>
 struct ManyShape {
     static constexpr int kStageBytes = kTileBytes + BN * kBlockK;
-    static constexpr int kTmemCols = 2 * BN;
-    static constexpr int kThreads = 320;
-    static constexpr int kCols = BN / 2;  // columns of a thread
-    static int smem_bytes(int stages) { return 1024 + stages * kStageBytes; }
+    static constexpr int kBufs = 512 / BN < 4 ? 512 / BN : 4;
+    static constexpr int kTmemCols = kBufs * BN;
+    static constexpr int kPromotionWarps = 8;
+    static constexpr int kThreads = 96 + kPromotionWarps * 32;
+    static constexpr int kCols = BN / (kPromotionWarps / 4);  // columns of a thread
+    static constexpr int kChunk = 16;                         // columns of a load from tensor memory
+    static constexpr int kScaleFloats = 128 + 4;              // of a stage: 128 rows of A, up to 2 blocks of W
+    static int smem_bytes(int stages) { return 1024 + stages * (kStageBytes + kScaleFloats * 4); }
 };
 
+// N consecutive values to a row of y whose alignment is p.out_align (32 or 16).
+template <int N>
+__device__ __forceinline__ void store_row(const GemmParams& p, int64_t at, const float (&v)[N]) {
+    if (p.out_type == kF32) {
+        float* y = static_cast<float*>(p.y) + at;
+#pragma unroll
+        for (int j = 0; j < N; j += 8)
+            st_global_32b(y + j, pack2(v[j], v[j + 1]), pack2(v[j + 2], v[j + 3]), pack2(v[j + 4], v[j + 5]),
+                          pack2(v[j + 6], v[j + 7]), p.out_align);
+    } else {
+        uint16_t* y = static_cast<uint16_t*>(p.y) + at;
+#pragma unroll
+        for (int j = 0; j < N; j += 16) {
+            uint32_t w[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                if (p.out_type == kF16) {
+                    const __half2 h = __floats2half2_rn(v[j + 2 * i], v[j + 2 * i + 1]);
+                    w[i] = *reinterpret_cast<const uint32_t*>(&h);
+                } else {
+                    const __nv_bfloat162 h = __floats2bfloat162_rn(v[j + 2 * i], v[j + 2 * i + 1]);
+                    w[i] = *reinterpret_cast<const uint32_t*>(&h);
+                }
+            }
+            st_global_32b(y + j, pack2u(w[0], w[1]), pack2u(w[2], w[3]), pack2u(w[4], w[5]), pack2u(w[6], w[7]),
+                          p.out_align);
+        }
+    }
+}
+
 template <int BN>
-__global__ void __launch_bounds__(320, 1) fp8_gemm_many_kernel(const __grid_constant__ CUtensorMap map_w,
-                                                                const __grid_constant__ CUtensorMap map_a,
-                                                                const GemmParams p) {
+__global__ void __launch_bounds__(ManyShape<BN>::kThreads, 1) fp8_gemm_many_kernel(
+    const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_a, const GemmParams p) {
     using S = ManyShape<BN>;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ uint64_t full[kMaxStages], empty[kMaxStages], tfull[2], tempty[2];
+    __shared__ uint64_t full[kMaxStages], empty[kMaxStages], tfull[S::kBufs], tempty[S::kBufs];
     __shared__ uint32_t taddr_s;
     __shared__ int dead_s;
     uint8_t* ring = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+    float* scales = reinterpret_cast<float*>(ring + p.stages * S::kStageBytes);
     volatile int* dead = &dead_s;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n;
@@ -499,12 +535,12 @@ __global__ void __launch_bounds__(320, 1) fp8_gemm_many_kernel(const __grid_cons
     if (threadIdx.x == 0) {
         dead_s = 0;
         for (int i = 0; i < p.stages; ++i) {
-            mbar_init(&full[i], 1);
-            mbar_init(&empty[i], 1);
+            mbar_init(&full[i], 1 + 32);
+            mbar_init(&empty[i], 1 + S::kPromotionWarps);
         }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < S::kBufs; ++i) {
             mbar_init(&tfull[i], 1);
-            mbar_init(&tempty[i], 8);
+            mbar_init(&tempty[i], S::kPromotionWarps);
         }
         fence_mbar_init();
         tma_prefetch_map(&map_w);
@@ -541,8 +577,8 @@ __global__ void __launch_bounds__(320, 1) fp8_gemm_many_kernel(const __grid_cons
             bool alive = true;
             for (int64_t tile = blockIdx.x; tile < tiles && alive; tile += gridDim.x) {
                 for (int kb = 0; kb < p.nkb; ++kb, ++it) {
-                    const int buf = it & 1;
-                    alive = wait_alive(&tempty[buf], ((it >> 1) & 1) ^ 1, dead) && wait_alive(&full[st], ph, dead);
+                    const int buf = it % S::kBufs;
+                    alive = wait_alive(&tempty[buf], ((it / S::kBufs) & 1) ^ 1, dead) && wait_alive(&full[st], ph, dead);
                     if (!alive) {
                         let_copies_land();
                         break;
@@ -556,86 +592,82 @@ __global__ void __launch_bounds__(320, 1) fp8_gemm_many_kernel(const __grid_cons
                 }
             }
         }
+    } else if (warp == 2) {
+        int st = 0, ph = 0;
+        bool alive = true;
+        const int w_blocks = (p.n + 127) / 128;
+        for (int64_t tile = blockIdx.x; tile < tiles && alive; tile += gridDim.x) {
+            const int tn = (int)(tile / p.tiles_m), tm = (int)(tile - (int64_t)tn * p.tiles_m);
+            for (int kb = 0; kb < p.nkb; ++kb) {
+                if (!(alive = __all_sync(0xffffffffu, wait_alive(&empty[st], ph ^ 1, dead)))) break;
+                float* dst = scales + st * S::kScaleFloats;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int row = tm * 128 + i * 32 + lane;
+                    cp_async4(dst + i * 32 + lane, p.sa + (row < p.m ? row * p.ld_sa + kb : 0), row < p.m);
+                }
+                const int wb = tn * BN / 128 + lane;
+                if (lane < (BN + 127) / 128)
+                    cp_async4(dst + 128 + lane, p.sw + (wb < w_blocks ? wb * p.ld_sw + kb : 0), wb < w_blocks);
+                cp_async_arrive(&full[st]);
+                if (++st == p.stages) st = 0, ph ^= 1;
+            }
+        }
     } else {
-        const int half = (warp - 2) / 4;
+        const int group = (warp - 3) / 4;
         const int r = (warp & 3) * 32 + lane;
-        const uint32_t lanes = taddr + ((uint32_t)(warp & 3) << 21) + half * S::kCols;
+        const uint32_t lanes = taddr + ((uint32_t)(warp & 3) << 21) + group * S::kCols;
         uint32_t it = 0;
+        int st = 0, ph = 0;
         bool alive = true;
         for (int64_t tile = blockIdx.x; tile < tiles && alive; tile += gridDim.x) {
             const int tn = (int)(tile / p.tiles_m), tm = (int)(tile - (int64_t)tn * p.tiles_m);
             const int64_t row = (int64_t)tm * 128 + r;
-            const int col0 = tn * BN + half * S::kCols;
+            const int col0 = tn * BN + group * S::kCols;
             const bool row_ok = row < p.m;
-            const float* sa = p.sa + (row_ok ? row : 0) * p.ld_sa;
-            // the columns of a thread lie in one 128-row block of W
-            const float* sw = p.sw + (int64_t)min(col0 / 128, (p.n - 1) / 128) * p.ld_sw;
-            uint64_t acc[S::kCols / 2];
+            float acc[S::kCols];
 #pragma unroll
-            for (int j = 0; j < S::kCols / 2; ++j) acc[j] = 0;
-            float s_next = __ldg(sa) * __ldg(sw);
+            for (int j = 0; j < S::kCols; ++j) acc[j] = 0.f;
             for (int kb = 0; kb < p.nkb; ++kb, ++it) {
-                const int buf = it & 1;
-                const float s = s_next;
-                if (kb + 1 < p.nkb) s_next = __ldg(sa + kb + 1) * __ldg(sw + kb + 1);
-                if (!(alive = __all_sync(0xffffffffu, wait_alive(&tfull[buf], (it >> 1) & 1, dead)))) break;
+                const int buf = it % S::kBufs;
+                alive = wait_alive(&full[st], ph, dead) && wait_alive(&tfull[buf], (it / S::kBufs) & 1, dead);
+                if (!(alive = __all_sync(0xffffffffu, alive))) break;
                 tc_fence_after();
-                const uint64_t ss = pack2(s, s);
-                uint32_t d[2][16];
-                tmem_ld16(lanes + buf * BN, d[0]);
+                // the columns of a thread lie in one 128-row block of W
+                const float* sc = scales + st * S::kScaleFloats;
+                const float s = sc[r] * sc[128 + group * S::kCols / 128];
+                uint32_t d[2][S::kChunk];
+                tmem_ld(lanes + buf * BN, d[0]);
 #pragma unroll
-                for (int c = 0; c < S::kCols / 16; ++c) {
+                for (int c = 0; c < S::kCols / S::kChunk; ++c) {
                     tmem_wait_ld(d[c & 1]);
-                    if (c + 1 < S::kCols / 16) tmem_ld16(lanes + buf * BN + (c + 1) * 16, d[(c + 1) & 1]);
+                    if (c + 1 < S::kCols / S::kChunk) {
+                        tmem_ld(lanes + buf * BN + (c + 1) * S::kChunk, d[(c + 1) & 1]);
+                    } else {  // the accumulator and the scales are read
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) {
+                            mbar_arrive(&tempty[buf]);
+                            mbar_arrive(&empty[st]);
+                        }
+                    }
 #pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        fma2(acc[c * 8 + j], pack2u(d[c & 1][2 * j], d[c & 1][2 * j + 1]), ss);
+                    for (int j = 0; j < S::kChunk; ++j) {
+                        float& v = acc[c * S::kChunk + j];
+                        v = fmaf(__uint_as_float(d[c & 1][j]), s, v);
+                    }
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&tempty[buf]);
+                if (++st == p.stages) st = 0, ph ^= 1;
             }
             if (!alive || !row_ok) continue;
             const int64_t at = row * p.ldy + col0;
             const int left = p.n - col0;
-            if (p.vec_out && left >= S::kCols) {
-                if (p.out_type == kF32) {
-                    float4* y = reinterpret_cast<float4*>(static_cast<float*>(p.y) + at);
-#pragma unroll
-                    for (int j = 0; j < S::kCols / 4; ++j) {
-                        float4 v;
-                        unpack2(acc[2 * j], v.x, v.y);
-                        unpack2(acc[2 * j + 1], v.z, v.w);
-                        y[j] = v;
-                    }
-                } else {
-                    uint4* y = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.y) + at);
-#pragma unroll
-                    for (int j = 0; j < S::kCols / 8; ++j) {
-                        uint32_t w[4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            float lo, hi;
-                            unpack2(acc[4 * j + i], lo, hi);
-                            if (p.out_type == kF16) {
-                                const __half2 h = __floats2half2_rn(lo, hi);
-                                w[i] = *reinterpret_cast<const uint32_t*>(&h);
-                            } else {
-                                const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-                                w[i] = *reinterpret_cast<const uint32_t*>(&h);
-                            }
-                        }
-                        y[j] = make_uint4(w[0], w[1], w[2], w[3]);
-                    }
-                }
+            if (p.out_align >= 16 && left >= S::kCols) {
+                store_row<S::kCols>(p, at, acc);
             } else {
 #pragma unroll
-                for (int j = 0; j < S::kCols / 2; ++j) {
-                    float lo, hi;
-                    unpack2(acc[j], lo, hi);
-                    if (2 * j < left) store_out(p.y, at + 2 * j, p.out_type, lo);
-                    if (2 * j + 1 < left) store_out(p.y, at + 2 * j + 1, p.out_type, hi);
-                }
+                for (int j = 0; j < S::kCols; ++j)
+                    if (j < left) store_out(p.y, at + j, p.out_type, acc[j]);
             }
         }
     }

@@ -98,7 +98,7 @@ sqz_status launch_many(const CUtensorMap& mw, const CUtensorMap& ma, GemmParams 
     if (st != SQZ_OK) return st;
     p.tiles_m = (p.m + 127) / 128;
     p.tiles_n = (p.n + BN - 1) / BN;
-    int stages = (d.smem - 2048) / ManyShape<BN>::kStageBytes;
+    const int stages = (d.smem - 2048) / (ManyShape<BN>::kStageBytes + ManyShape<BN>::kScaleFloats * 4);
     p.stages = stages > 8 ? 8 : stages;
     const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n;
     cudaLaunchConfig_t cfg = {};
@@ -224,7 +224,9 @@ extern "C" SQZ_API sqz_status sqz_fp8_gemm(const sqz_fp8_matrix* a, const sqz_fp
     p.n = n;
     p.nkb = (k + 127) / 128;
     p.out_type = y_type;
-    p.vec_out = reinterpret_cast<uintptr_t>(y) % 16 == 0 && ldy * out_bytes % 16 == 0;
+    p.out_align = 32;
+    while (p.out_align > 2 && (reinterpret_cast<uintptr_t>(y) % p.out_align || ldy * out_bytes % p.out_align))
+        p.out_align /= 2;
     if ((st = status_word(&p.status)) != SQZ_OK) return st;
     CUtensorMap mw, ma;
     const int64_t row_blocks = ((int64_t)n + 127) / 128;
