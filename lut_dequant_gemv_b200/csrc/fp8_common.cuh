@@ -65,6 +65,21 @@ __device__ __forceinline__ bool wait_alive(uint64_t* bar, uint32_t parity, volat
     return mbar_poll(bar, parity) || wait_long(bar, parity, dead);
 }
 
+// A whole warp's wait; the answer is the same in every lane, and the compiler
+// sees that it is.  The roles that issue copies and matrix instructions run
+// their loops with all lanes and elect one for the instruction itself: their
+// operands then stay in uniform registers.  (Under `if (lane == 0)` each operand
+// is moved there first: four matrix instructions took over 300 cycles to issue.)
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volatile int* dead) {
+    return __all_sync(0xffffffffu, wait_alive(bar, parity, dead));
+}
+__device__ __forceinline__ bool elect_one() {
+    uint32_t one;
+    asm volatile(
+        "{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(one));
+    return one != 0;
+}
+
 // After a wait gave up: time (100 ms) for the thread's own copies and matrix
 // instructions in flight to end before the CTA frees its memory and leaves.
 __device__ __forceinline__ void let_copies_land() {
@@ -137,6 +152,36 @@ __device__ __forceinline__ void mma_block(uint32_t d, uint32_t a_addr, uint32_t 
     const uint64_t a = operand_desc(a_addr), b = operand_desc(b_addr);
 #pragma unroll
     for (int k = 0; k < 4; ++k) mma_f8(d, a + 2 * k, b + 2 * k, idesc, k > 0);
+}
+// The same across a pair of CTAs (cta_group::2), issued by one thread of the
+// even one: M = 256, each CTA's tensor memory gets the 128 rows of its A tile;
+// the tiles lie at the same shared-memory addresses in both CTAs, each with
+// half of B's rows.
+__device__ __forceinline__ void mma_block_pair(uint32_t d, uint32_t a_addr, uint32_t b_addr, uint32_t idesc) {
+    const uint64_t a = operand_desc(a_addr), b = operand_desc(b_addr);
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        asm volatile(
+            "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+            " tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+            "l"(a + 2 * k), "l"(b + 2 * k), "r"(idesc), "r"(k > 0 ? 1 : 0)
+            : "memory");
+}
+// One arrival on `bar` of both CTAs of the pair.
+__device__ __forceinline__ void mma_commit_pair(uint64_t* bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            smem_u32(bar)),
+        "h"((uint16_t)3)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_alloc_pair(uint32_t* dst, uint32_t cols) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst)), "r"(cols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t cols) {
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(cols) : "memory");
 }
 // One arrival on `bar` when the thread's matrix instructions so far are done.
 __device__ __forceinline__ void mma_commit(uint64_t* bar) {
@@ -230,6 +275,26 @@ __device__ __forceinline__ uint64_t fma2_of(uint64_t a, uint64_t b, uint64_t c) 
 }
 
 // -------------------------------------------------------------- clusters
+// The address in the cluster's window of a shared-memory address of CTA `rank`.
+__device__ __forceinline__ uint32_t cluster_addr(const void* p, uint32_t rank) {
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+    return a;
+}
+// A tile load whose bytes are counted on a barrier of the pair's even CTA.
+__device__ __forceinline__ void tma_load_2d_pair(void* dst, const CUtensorMap* map, uint32_t bar, int x, int y) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], "
+        "[%1, {%3, %4}], [%2];" ::"r"(smem_u32(dst)),
+        "l"(map), "r"(bar), "r"(x), "r"(y)
+        : "memory");
+}
+// An arrival on another CTA's barrier.  What it tells about (tensor memory is
+// read, a stage is free) is ordered by tcgen05 fences and copies' own
+// completion: no fence at cluster scope, which costs over a thousand cycles.
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));

@@ -279,6 +279,7 @@ struct GemmParams {
     uint32_t idesc;
     int stages;
     int tiles_m, tiles_n;  // many-row kernel
+    int vec_sa, vec_sw;    // rows of scales are 16-byte aligned
     int out_align;         // alignment of y's rows in bytes: 32, 16 or less
 };
 
@@ -352,35 +353,35 @@ __global__ void __launch_bounds__(224) fp8_gemm_few_kernel(const __grid_constant
 
     float acc[TB];
     if (warp == 0) {
-        if (lane == 0) {
-            int st = 0, ph = 0, it = 0;
-            for (; it < nk; ++it) {
-                if (!wait_alive(&empty[st], ph ^ 1, dead)) break;
+        int st = 0, ph = 0, it = 0;
+        for (; it < nk; ++it) {
+            if (!wait_warp(&empty[st], ph ^ 1, dead)) break;
+            uint8_t* at = ring + st * S::kStageBytes;
+            if (elect_one()) {
                 mbar_expect_tx(&full[st], S::kStageBytes);
-                uint8_t* at = ring + st * S::kStageBytes;
                 tma_load_2d(at, &map_w, &full[st], (kb0 + it) * kBlockK, row0);
                 tma_load_2d(at + kTileBytes, &map_a, &full[st], (kb0 + it) * kBlockK, tok0);
-                if (++st == p.stages) st = 0, ph ^= 1;
             }
-            if (it < nk) let_copies_land();
+            __syncwarp();
+            if (++st == p.stages) st = 0, ph ^= 1;
         }
+        if (it < nk) let_copies_land();
     } else if (warp == 1) {
-        if (lane == 0) {
-            int st = 0, ph = 0;
-            for (int it = 0; it < nk; ++it) {
-                const int buf = it % S::kBufs;
-                if (!wait_alive(&tempty[buf], ((it / S::kBufs) & 1) ^ 1, dead) || !wait_alive(&full[st], ph, dead)) {
-                    let_copies_land();
-                    break;
-                }
-                tc_fence_after();
-                const uint32_t at = smem_u32(ring + st * S::kStageBytes);
+        int st = 0, ph = 0, it = 0;
+        for (; it < nk; ++it) {
+            const int buf = it % S::kBufs;
+            if (!wait_warp(&tempty[buf], ((it / S::kBufs) & 1) ^ 1, dead) || !wait_warp(&full[st], ph, dead)) break;
+            tc_fence_after();
+            const uint32_t at = smem_u32(ring + st * S::kStageBytes);
+            if (elect_one()) {
                 mma_block(taddr + buf * TB, at, at + kTileBytes, p.idesc);
-                mma_commit(&empty[st]);
                 mma_commit(&tfull[buf]);
-                if (++st == p.stages) st = 0, ph ^= 1;
+                mma_commit(&empty[st]);
             }
+            __syncwarp();
+            if (++st == p.stages) st = 0, ph ^= 1;
         }
+        if (it < nk) let_copies_land();
     } else if (warp == 2) {
         int st = 0, ph = 0;
         const float* sw = p.sw + (int64_t)blockIdx.y * p.ld_sw;
@@ -461,30 +462,34 @@ __global__ void __launch_bounds__(224) fp8_gemm_few_kernel(const __grid_constant
     cluster_sync();  // the other CTAs have read this one's sums
 }
 
-// Many rows of A: bound by the tensor cores and by the promotion.  Tiles of
-// 128 rows of A x BN rows of W, a persistent CTA per SM.  A thread of the
-// promotion holds one row of A and BN / 4 columns: the block's scale is then
-// one number per thread (the row's scale times the scale of the 128 rows of W
-// that its columns lie in), and the multiply-adds go two to an instruction.
-// Accumulators in tensor memory take turns (two of 256 columns), so that the
-// matrix instructions of block b + 1 run under the promotion of block b; with
-// sixteen warps the promotion's loads from tensor memory overlap each other
-// (eight warps of 16-column loads took 1170 cycles a block, where the matrix
-// instructions take 512).
+// Many rows of A: tiles of 256 rows of A x BN rows of W, by pairs of CTAs (one
+// CTA an SM, persistent).  What bounds a tile is first the way from L2: alone,
+// a CTA with a 128 x 256 tile takes 48 KB a block of K for 512 cycles of matrix
+// instructions and the SMs together get about 10 TB/s, which made a block take
+// over 1100 cycles whatever the promotion did.  In a pair each CTA loads its
+// own 128 rows of A and half of W's rows, 32 KB for the same work, and the
+// matrix instructions (cta_group::2) read W's halves from both.
 //
-//   warp 0: TMA ring, warp 1: TMEM and matrix instructions, warps 2-17:
-//   promotion (warp % 4 = the 32 lanes it may read; a quarter of the columns)
+// A thread of the promotion holds one row of A and BN / 2 columns: the block's
+// scale is then one number per thread (the row's scale times the scale of the
+// 128 rows of W that its columns lie in).  (Packed fp32 multiply-adds measured
+// slower here than plain ones.)
+//
+//   warp 0: TMA ring (the full barriers live in the even CTA, the empty ones
+//   in both), warp 1: TMEM and, in the even CTA, matrix instructions, warp 2:
+//   idle, warps 3-10: promotion (warp % 4 = the 32 lanes it may read; first or
+//   second half of the columns)
 template <int BN>
 struct ManyShape {
-    static constexpr int kStageBytes = kTileBytes + BN * kBlockK;
-    static constexpr int kBufs = 512 / BN < 4 ? 512 / BN : 4;
+    static constexpr int kRowsW = BN / 2;  // of W, in each CTA
+    static constexpr int kStageBytes = kTileBytes + kRowsW * kBlockK;
+    static constexpr int kBufs = 512 / BN < 4 ? 512 / BN : 4;  // accumulators that take turns
     static constexpr int kTmemCols = kBufs * BN;
     static constexpr int kPromotionWarps = 8;
     static constexpr int kThreads = 96 + kPromotionWarps * 32;
-    static constexpr int kCols = BN / (kPromotionWarps / 4);  // columns of a thread
-    static constexpr int kChunk = 16;                         // columns of a load from tensor memory
-    static constexpr int kScaleFloats = 128 + 4;              // of a stage: 128 rows of A, up to 2 blocks of W
-    static int smem_bytes(int stages) { return 1024 + stages * (kStageBytes + kScaleFloats * 4); }
+    static constexpr int kCols = BN / 2;   // columns of a thread
+    static constexpr int kChunk = 16;      // columns of a load from tensor memory
+    static int smem_bytes(int stages) { return 1024 + stages * kStageBytes; }
 };
 
 // N consecutive values to a row of y whose alignment is p.out_align (32 or 16).
@@ -517,6 +522,13 @@ __device__ __forceinline__ void store_row(const GemmParams& p, int64_t at, const
     }
 }
 
+// p[i .. i + 3], zeros from `end` on; `vec`: p is 16-byte aligned.
+__device__ __forceinline__ float4 load4(const float* p, int i, int end, bool vec) {
+    if (vec && i + 4 <= end) return __ldg(reinterpret_cast<const float4*>(p + i));
+    return make_float4(i < end ? __ldg(p + i) : 0.f, i + 1 < end ? __ldg(p + i + 1) : 0.f,
+                       i + 2 < end ? __ldg(p + i + 2) : 0.f, i + 3 < end ? __ldg(p + i + 3) : 0.f);
+}
+
 template <int BN>
 __global__ void __launch_bounds__(ManyShape<BN>::kThreads, 1) fp8_gemm_many_kernel(
     const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_a, const GemmParams p) {
@@ -526,21 +538,21 @@ __global__ void __launch_bounds__(ManyShape<BN>::kThreads, 1) fp8_gemm_many_kern
     __shared__ uint32_t taddr_s;
     __shared__ int dead_s;
     uint8_t* ring = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
-    float* scales = reinterpret_cast<float*>(ring + p.stages * S::kStageBytes);
     volatile int* dead = &dead_s;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int rank = (int)cluster_rank(), pair = blockIdx.x / 2, pairs = gridDim.x / 2;
     const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n;
 
-    if (warp == 1) tmem_alloc(&taddr_s, S::kTmemCols);
+    if (warp == 1) tmem_alloc_pair(&taddr_s, S::kTmemCols);
     if (threadIdx.x == 0) {
         dead_s = 0;
         for (int i = 0; i < p.stages; ++i) {
-            mbar_init(&full[i], 1 + 32);
-            mbar_init(&empty[i], 1 + S::kPromotionWarps);
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], 1);
         }
         for (int i = 0; i < S::kBufs; ++i) {
             mbar_init(&tfull[i], 1);
-            mbar_init(&tempty[i], S::kPromotionWarps);
+            mbar_init(&tempty[i], 2 * S::kPromotionWarps);
         }
         fence_mbar_init();
         tma_prefetch_map(&map_w);
@@ -548,94 +560,91 @@ __global__ void __launch_bounds__(ManyShape<BN>::kThreads, 1) fp8_gemm_many_kern
     }
     tc_fence_before();
     __syncthreads();
+    cluster_sync();  // the other CTA's barriers are ready
     tc_fence_after();
     const uint32_t taddr = taddr_s;
     pdl_launch_dependents();
     pdl_wait_previous();
 
     if (warp == 0) {
-        if (lane == 0) {
+        int st = 0, ph = 0;
+        bool alive = true;
+        const uint32_t leader_full = cluster_addr(full, 0);
+        for (int64_t tile = pair; tile < tiles && alive; tile += pairs) {
+            const int tn = (int)(tile / p.tiles_m), tm = (int)(tile - (int64_t)tn * p.tiles_m);
+            for (int kb = 0; kb < p.nkb; ++kb) {
+                if (!(alive = wait_warp(&empty[st], ph ^ 1, dead))) break;
+                const uint32_t bar = leader_full + st * 8;
+                uint8_t* at = ring + st * S::kStageBytes;
+                if (elect_one()) {
+                    if (rank == 0) mbar_expect_tx(&full[st], 2 * S::kStageBytes);
+                    tma_load_2d_pair(at, &map_a, bar, kb * kBlockK, tm * 256 + rank * 128);
+                    tma_load_2d_pair(at + kTileBytes, &map_w, bar, kb * kBlockK, tn * BN + rank * S::kRowsW);
+                }
+                __syncwarp();
+                if (++st == p.stages) st = 0, ph ^= 1;
+            }
+        }
+        // The last arrivals on this CTA's empty barriers come from the even CTA:
+        // they are here before this one leaves.
+        for (int i = 0; i < p.stages && alive; ++i) {
+            alive = wait_warp(&empty[st], ph ^ 1, dead);
+            if (++st == p.stages) st = 0, ph ^= 1;
+        }
+        if (!alive) let_copies_land();
+    } else if (warp == 1) {
+        if (rank == 0) {
             int st = 0, ph = 0;
+            uint32_t it = 0;
             bool alive = true;
-            for (int64_t tile = blockIdx.x; tile < tiles && alive; tile += gridDim.x) {
-                const int tn = (int)(tile / p.tiles_m), tm = (int)(tile - (int64_t)tn * p.tiles_m);
-                for (int kb = 0; kb < p.nkb; ++kb) {
-                    if (!(alive = wait_alive(&empty[st], ph ^ 1, dead))) break;
-                    mbar_expect_tx(&full[st], S::kStageBytes);
-                    uint8_t* at = ring + st * S::kStageBytes;
-                    tma_load_2d(at, &map_a, &full[st], kb * kBlockK, tm * 128);
-                    tma_load_2d(at + kTileBytes, &map_w, &full[st], kb * kBlockK, tn * BN);
+            for (int64_t tile = pair; tile < tiles && alive; tile += pairs) {
+                for (int kb = 0; kb < p.nkb; ++kb, ++it) {
+                    const int buf = it % S::kBufs;
+                    alive = wait_warp(&tempty[buf], ((it / S::kBufs) & 1) ^ 1, dead) && wait_warp(&full[st], ph, dead);
+                    if (!alive) break;
+                    tc_fence_after();
+                    const uint32_t at = smem_u32(ring + st * S::kStageBytes);
+                    if (elect_one()) {
+                        mma_block_pair(taddr + buf * BN, at, at + kTileBytes, p.idesc);
+                        mma_commit_pair(&tfull[buf]);
+                        mma_commit_pair(&empty[st]);
+                    }
+                    __syncwarp();
                     if (++st == p.stages) st = 0, ph ^= 1;
                 }
             }
             if (!alive) let_copies_land();
         }
-    } else if (warp == 1) {
-        if (lane == 0) {
-            int st = 0, ph = 0;
-            uint32_t it = 0;
-            bool alive = true;
-            for (int64_t tile = blockIdx.x; tile < tiles && alive; tile += gridDim.x) {
-                for (int kb = 0; kb < p.nkb; ++kb, ++it) {
-                    const int buf = it % S::kBufs;
-                    alive = wait_alive(&tempty[buf], ((it / S::kBufs) & 1) ^ 1, dead) && wait_alive(&full[st], ph, dead);
-                    if (!alive) {
-                        let_copies_land();
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint32_t at = smem_u32(ring + st * S::kStageBytes);
-                    mma_block(taddr + buf * BN, at, at + kTileBytes, p.idesc);
-                    mma_commit(&empty[st]);
-                    mma_commit(&tfull[buf]);
-                    if (++st == p.stages) st = 0, ph ^= 1;
-                }
-            }
-        }
-    } else if (warp == 2) {
-        int st = 0, ph = 0;
-        bool alive = true;
-        const int w_blocks = (p.n + 127) / 128;
-        for (int64_t tile = blockIdx.x; tile < tiles && alive; tile += gridDim.x) {
-            const int tn = (int)(tile / p.tiles_m), tm = (int)(tile - (int64_t)tn * p.tiles_m);
-            for (int kb = 0; kb < p.nkb; ++kb) {
-                if (!(alive = __all_sync(0xffffffffu, wait_alive(&empty[st], ph ^ 1, dead)))) break;
-                float* dst = scales + st * S::kScaleFloats;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int row = tm * 128 + i * 32 + lane;
-                    cp_async4(dst + i * 32 + lane, p.sa + (row < p.m ? row * p.ld_sa + kb : 0), row < p.m);
-                }
-                const int wb = tn * BN / 128 + lane;
-                if (lane < (BN + 127) / 128)
-                    cp_async4(dst + 128 + lane, p.sw + (wb < w_blocks ? wb * p.ld_sw + kb : 0), wb < w_blocks);
-                cp_async_arrive(&full[st]);
-                if (++st == p.stages) st = 0, ph ^= 1;
-            }
-        }
-    } else {
+    } else if (warp > 2) {
         const int group = (warp - 3) / 4;
         const int r = (warp & 3) * 32 + lane;
         const uint32_t lanes = taddr + ((uint32_t)(warp & 3) << 21) + group * S::kCols;
+        const uint32_t leader_tempty = cluster_addr(tempty, 0);
         uint32_t it = 0;
-        int st = 0, ph = 0;
         bool alive = true;
-        for (int64_t tile = blockIdx.x; tile < tiles && alive; tile += gridDim.x) {
+        for (int64_t tile = pair; tile < tiles && alive; tile += pairs) {
             const int tn = (int)(tile / p.tiles_m), tm = (int)(tile - (int64_t)tn * p.tiles_m);
-            const int64_t row = (int64_t)tm * 128 + r;
+            const int64_t row = (int64_t)tm * 256 + rank * 128 + r;
             const int col0 = tn * BN + group * S::kCols;
-            const bool row_ok = row < p.m;
+            // the columns of a thread lie in one 128-row block of W
+            const float* sa = p.sa + (row < p.m ? row : 0) * p.ld_sa;
+            const float* sw = p.sw + (int64_t)min(col0 / 128, (p.n - 1) / 128) * p.ld_sw;
             float acc[S::kCols];
 #pragma unroll
             for (int j = 0; j < S::kCols; ++j) acc[j] = 0.f;
+            float4 a4 = load4(sa, 0, p.nkb, p.vec_sa), w4 = load4(sw, 0, p.nkb, p.vec_sw);
+            float4 s4 = make_float4(0.f, 0.f, 0.f, 0.f);
             for (int kb = 0; kb < p.nkb; ++kb, ++it) {
                 const int buf = it % S::kBufs;
-                alive = wait_alive(&full[st], ph, dead) && wait_alive(&tfull[buf], (it / S::kBufs) & 1, dead);
-                if (!(alive = __all_sync(0xffffffffu, alive))) break;
+                if ((kb & 3) == 0) {  // the next four blocks' scales are asked for four blocks ahead
+                    s4 = make_float4(a4.x * w4.x, a4.y * w4.y, a4.z * w4.z, a4.w * w4.w);
+                    a4 = load4(sa, kb + 4, p.nkb, p.vec_sa);
+                    w4 = load4(sw, kb + 4, p.nkb, p.vec_sw);
+                }
+                const float s = s4.x;
+                s4 = make_float4(s4.y, s4.z, s4.w, 0.f);
+                if (!(alive = wait_warp(&tfull[buf], (it / S::kBufs) & 1, dead))) break;
                 tc_fence_after();
-                // the columns of a thread lie in one 128-row block of W
-                const float* sc = scales + st * S::kScaleFloats;
-                const float s = sc[r] * sc[128 + group * S::kCols / 128];
                 uint32_t d[2][S::kChunk];
                 tmem_ld(lanes + buf * BN, d[0]);
 #pragma unroll
@@ -643,13 +652,10 @@ __global__ void __launch_bounds__(ManyShape<BN>::kThreads, 1) fp8_gemm_many_kern
                     tmem_wait_ld(d[c & 1]);
                     if (c + 1 < S::kCols / S::kChunk) {
                         tmem_ld(lanes + buf * BN + (c + 1) * S::kChunk, d[(c + 1) & 1]);
-                    } else {  // the accumulator and the scales are read
+                    } else {  // the accumulator is read
                         tc_fence_before();
                         __syncwarp();
-                        if (lane == 0) {
-                            mbar_arrive(&tempty[buf]);
-                            mbar_arrive(&empty[st]);
-                        }
+                        if (elect_one()) mbar_arrive_cluster(leader_tempty + buf * 8);
                     }
 #pragma unroll
                     for (int j = 0; j < S::kChunk; ++j) {
@@ -657,9 +663,8 @@ __global__ void __launch_bounds__(ManyShape<BN>::kThreads, 1) fp8_gemm_many_kern
                         v = fmaf(__uint_as_float(d[c & 1][j]), s, v);
                     }
                 }
-                if (++st == p.stages) st = 0, ph ^= 1;
             }
-            if (!alive || !row_ok) continue;
+            if (!alive || row >= p.m) continue;
             const int64_t at = row * p.ldy + col0;
             const int left = p.n - col0;
             if (p.out_align >= 16 && left >= S::kCols) {
@@ -673,8 +678,9 @@ __global__ void __launch_bounds__(ManyShape<BN>::kThreads, 1) fp8_gemm_many_kern
     }
     __syncwarp();  // one lane ran the role: the barrier counts whole warps
     __syncthreads();
+    cluster_sync();  // nothing of the other CTA is on its way here any more
     tc_fence_after();
-    if (warp == 1) tmem_dealloc(taddr, S::kTmemCols);
+    if (warp == 1) tmem_dealloc_pair(taddr, S::kTmemCols);
     if (threadIdx.x == 0 && *dead) atomicOr(p.status, 1);
 }
 

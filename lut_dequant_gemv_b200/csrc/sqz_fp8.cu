@@ -96,21 +96,24 @@ sqz_status launch_many(const CUtensorMap& mw, const CUtensorMap& ma, GemmParams 
     static std::atomic<uint64_t> ready;
     const sqz_status st = allow_smem(fp8_gemm_many_kernel<BN>, d, &ready);
     if (st != SQZ_OK) return st;
-    p.tiles_m = (p.m + 127) / 128;
+    p.tiles_m = (p.m + 255) / 256;
     p.tiles_n = (p.n + BN - 1) / BN;
-    const int stages = (d.smem - 2048) / (ManyShape<BN>::kStageBytes + ManyShape<BN>::kScaleFloats * 4);
+    const int stages = (d.smem - 2048 - ManyShape<BN>::smem_bytes(0)) / ManyShape<BN>::kStageBytes;
     p.stages = stages > 8 ? 8 : stages;
-    const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n;
+    const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n, pairs = d.sms / 2;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(tiles < d.sms ? tiles : d.sms));
+    cfg.gridDim = dim3((unsigned)(2 * (tiles < pairs ? tiles : pairs)));
     cfg.blockDim = dim3(ManyShape<BN>::kThreads);
     cfg.dynamicSmemBytes = (size_t)ManyShape<BN>::smem_bytes(p.stages);
     cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 2;
     SQZ_F8_TRY(cudaLaunchKernelEx(&cfg, fp8_gemm_many_kernel<BN>, mw, ma, p), "fp8 product launch");
     return SQZ_OK;
 }
@@ -224,6 +227,8 @@ extern "C" SQZ_API sqz_status sqz_fp8_gemm(const sqz_fp8_matrix* a, const sqz_fp
     p.n = n;
     p.nkb = (k + 127) / 128;
     p.out_type = y_type;
+    p.vec_sa = reinterpret_cast<uintptr_t>(p.sa) % 16 == 0 && p.ld_sa % 4 == 0;
+    p.vec_sw = reinterpret_cast<uintptr_t>(p.sw) % 16 == 0 && p.ld_sw % 4 == 0;
     p.out_align = 32;
     while (p.out_align > 2 && (reinterpret_cast<uintptr_t>(y) % p.out_align || ldy * out_bytes % p.out_align))
         p.out_align /= 2;
@@ -252,17 +257,17 @@ extern "C" SQZ_API sqz_status sqz_fp8_gemm(const sqz_fp8_matrix* a, const sqz_fp
         }
     }
     // The widest tile costs least per output; narrower ones when they need
-    // fewer rounds of the SMs (weights: measured time of a tile's block of K).
-    const int64_t tm = (m + 127) / 128;
+    // fewer rounds of the pairs of SMs (weights: measured time of a tile's block of K).
+    const int64_t tm = (m + 255) / 256, pairs = d.sms / 2;
     const auto rounds = [&](int bn, double weight) {
         const int64_t tiles = tm * (((int64_t)n + bn - 1) / bn);
-        return (double)((tiles + d.sms - 1) / d.sms) * weight;
+        return (double)((tiles + pairs - 1) / pairs) * weight;
     };
-    const double c256 = rounds(256, 1.0), c128 = rounds(128, 0.55), c64 = rounds(64, 0.4);
+    const double c256 = rounds(256, 1.0), c128 = rounds(128, 0.6), c64 = rounds(64, 0.45);
     const int bn = c256 <= c128 && c256 <= c64 ? 256 : c128 <= c64 ? 128 : 64;
-    if ((st = tile_map(&mw, w->q, k, n, w->ld, bn)) != SQZ_OK) return st;
+    if ((st = tile_map(&mw, w->q, k, n, w->ld, bn / 2)) != SQZ_OK) return st;
     if ((st = tile_map(&ma, a->q, k, m, a->ld, 128)) != SQZ_OK) return st;
-    p.idesc = instr_desc(a->format, w->format, 128, bn);
+    p.idesc = instr_desc(a->format, w->format, 256, bn);
     switch (bn) {
         case 256: return launch_many<256>(mw, ma, p, d, s);
         case 128: return launch_many<128>(mw, ma, p, d, s);
