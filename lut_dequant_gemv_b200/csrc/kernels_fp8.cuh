@@ -370,7 +370,7 @@ __global__ void __launch_bounds__(224) fp8_gemm_few_kernel(const __grid_constant
         int st = 0, ph = 0, it = 0;
         for (; it < nk; ++it) {
             const int buf = it % S::kBufs;
-            if (!wait_warp(&tempty[buf], ((it / S::kBufs) & 1) ^ 1, dead) || !wait_warp(&full[st], ph, dead)) break;
+            if (!wait_warp(&full[st], ph, dead) || !wait_warp(&tempty[buf], ((it / S::kBufs) & 1) ^ 1, dead)) break;
             tc_fence_after();
             const uint32_t at = smem_u32(ring + st * S::kStageBytes);
             if (elect_one()) {
@@ -477,7 +477,9 @@ __global__ void __launch_bounds__(224) fp8_gemm_few_kernel(const __grid_constant
 //
 //   warp 0: TMA ring (the full barriers live in the even CTA, the empty ones
 //   in both), warp 1: TMEM and, in the even CTA, matrix instructions, warp 2:
-//   idle, warps 3-10: promotion (warp % 4 = the 32 lanes it may read; first or
+//   scales, sixteen blocks of K ahead (a wait for each block's would cost the
+//   promotion 200 cycles of its 1000; loads into its registers stall its reads
+//   of tensor memory), warps 3-10: promotion (warp % 4 = the 32 lanes it may read; first or
 //   second half of the columns)
 template <int BN>
 struct ManyShape {
@@ -489,7 +491,10 @@ struct ManyShape {
     static constexpr int kThreads = 96 + kPromotionWarps * 32;
     static constexpr int kCols = BN / 2;   // columns of a thread
     static constexpr int kChunk = 16;      // columns of a load from tensor memory
-    static int smem_bytes(int stages) { return 1024 + stages * kStageBytes; }
+    // scales of kScaleRun blocks of K at a time, [four blocks][128 rows of A, 2 for W][4]
+    static constexpr int kScaleRun = 16;
+    static constexpr int kScaleRows = 128 + 2;
+    static int smem_bytes(int stages) { return 1024 + stages * kStageBytes + 2 * kScaleRun * kScaleRows * 4; }
 };
 
 // N consecutive values to a row of y whose alignment is p.out_align (32 or 16).
@@ -522,11 +527,15 @@ __device__ __forceinline__ void store_row(const GemmParams& p, int64_t at, const
     }
 }
 
-// p[i .. i + 3], zeros from `end` on; `vec`: p is 16-byte aligned.
-__device__ __forceinline__ float4 load4(const float* p, int i, int end, bool vec) {
-    if (vec && i + 4 <= end) return __ldg(reinterpret_cast<const float4*>(p + i));
-    return make_float4(i < end ? __ldg(p + i) : 0.f, i + 1 < end ? __ldg(p + i + 1) : 0.f,
-                       i + 2 < end ? __ldg(p + i + 2) : 0.f, i + 3 < end ? __ldg(p + i + 3) : 0.f);
+// Up to four consecutive scales to shared memory, asynchronously (in one copy
+// where the row is 16-byte aligned and four are left: a copy costs a line of L1
+// per lane whatever its width).
+__device__ __forceinline__ void copy_scales(float* dst, const float* src, int n, bool vec) {
+    if (vec && n == 4) {
+        tc::cp_async16(dst, src);
+    } else {
+        for (int i = 0; i < n; ++i) cp_async4(dst + i, src + i, true);
+    }
 }
 
 template <int BN>
@@ -535,9 +544,11 @@ __global__ void __launch_bounds__(ManyShape<BN>::kThreads, 1) fp8_gemm_many_kern
     using S = ManyShape<BN>;
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint64_t full[kMaxStages], empty[kMaxStages], tfull[S::kBufs], tempty[S::kBufs];
+    __shared__ uint64_t sfull[2], sempty[2];
     __shared__ uint32_t taddr_s;
     __shared__ int dead_s;
     uint8_t* ring = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+    float* scales = reinterpret_cast<float*>(ring + p.stages * S::kStageBytes);
     volatile int* dead = &dead_s;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int rank = (int)cluster_rank(), pair = blockIdx.x / 2, pairs = gridDim.x / 2;
@@ -553,6 +564,10 @@ __global__ void __launch_bounds__(ManyShape<BN>::kThreads, 1) fp8_gemm_many_kern
         for (int i = 0; i < S::kBufs; ++i) {
             mbar_init(&tfull[i], 1);
             mbar_init(&tempty[i], 2 * S::kPromotionWarps);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sfull[i], 32);
+            mbar_init(&sempty[i], S::kPromotionWarps);
         }
         fence_mbar_init();
         tma_prefetch_map(&map_w);
@@ -600,7 +615,8 @@ __global__ void __launch_bounds__(ManyShape<BN>::kThreads, 1) fp8_gemm_many_kern
             for (int64_t tile = pair; tile < tiles && alive; tile += pairs) {
                 for (int kb = 0; kb < p.nkb; ++kb, ++it) {
                     const int buf = it % S::kBufs;
-                    alive = wait_warp(&tempty[buf], ((it / S::kBufs) & 1) ^ 1, dead) && wait_warp(&full[st], ph, dead);
+                    // (the stage first: it is there long before the accumulator is free)
+                    alive = wait_warp(&full[st], ph, dead) && wait_warp(&tempty[buf], ((it / S::kBufs) & 1) ^ 1, dead);
                     if (!alive) break;
                     tc_fence_after();
                     const uint32_t at = smem_u32(ring + st * S::kStageBytes);
@@ -615,53 +631,72 @@ __global__ void __launch_bounds__(ManyShape<BN>::kThreads, 1) fp8_gemm_many_kern
             }
             if (!alive) let_copies_land();
         }
-    } else if (warp > 2) {
+    } else if (warp == 2) {
+        uint32_t runs = 0;
+        bool alive = true;
+        const int w_blocks = (p.n + 127) / 128;
+        for (int64_t tile = pair; tile < tiles && alive; tile += pairs) {
+            const int tn = (int)(tile / p.tiles_m), tm = (int)(tile - (int64_t)tn * p.tiles_m);
+            for (int k0 = 0; k0 < p.nkb; k0 += S::kScaleRun, ++runs) {
+                if (!(alive = wait_warp(&sempty[runs & 1], ((runs >> 1) & 1) ^ 1, dead))) break;
+                float* dst = scales + (runs & 1) * S::kScaleRun * S::kScaleRows;
+                const int wb = min(tn * BN / 128 + lane, w_blocks - 1);
+                for (int k = k0; k < min(k0 + S::kScaleRun, p.nkb); k += 4, dst += 4 * S::kScaleRows) {
+                    const int n = min(4, p.nkb - k);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int64_t row = min(tm * 256 + rank * 128 + i * 32 + lane, p.m - 1);
+                        copy_scales(dst + 4 * (i * 32 + lane), p.sa + row * p.ld_sa + k, n, p.vec_sa);
+                    }
+                    if (lane < (BN + 127) / 128)
+                        copy_scales(dst + 4 * (128 + lane), p.sw + wb * p.ld_sw + k, n, p.vec_sw);
+                }
+                cp_async_arrive(&sfull[runs & 1]);
+            }
+        }
+    } else {
         const int group = (warp - 3) / 4;
         const int r = (warp & 3) * 32 + lane;
         const uint32_t lanes = taddr + ((uint32_t)(warp & 3) << 21) + group * S::kCols;
         const uint32_t leader_tempty = cluster_addr(tempty, 0);
-        uint32_t it = 0;
+        uint32_t it = 0, runs = 0;
         bool alive = true;
         for (int64_t tile = pair; tile < tiles && alive; tile += pairs) {
             const int tn = (int)(tile / p.tiles_m), tm = (int)(tile - (int64_t)tn * p.tiles_m);
             const int64_t row = (int64_t)tm * 256 + rank * 128 + r;
             const int col0 = tn * BN + group * S::kCols;
-            // the columns of a thread lie in one 128-row block of W
-            const float* sa = p.sa + (row < p.m ? row : 0) * p.ld_sa;
-            const float* sw = p.sw + (int64_t)min(col0 / 128, (p.n - 1) / 128) * p.ld_sw;
             float acc[S::kCols];
 #pragma unroll
             for (int j = 0; j < S::kCols; ++j) acc[j] = 0.f;
-            float4 a4 = load4(sa, 0, p.nkb, p.vec_sa), w4 = load4(sw, 0, p.nkb, p.vec_sw);
-            float4 s4 = make_float4(0.f, 0.f, 0.f, 0.f);
+            const float* sc = nullptr;
             for (int kb = 0; kb < p.nkb; ++kb, ++it) {
                 const int buf = it % S::kBufs;
-                if ((kb & 3) == 0) {  // the next four blocks' scales are asked for four blocks ahead
-                    s4 = make_float4(a4.x * w4.x, a4.y * w4.y, a4.z * w4.z, a4.w * w4.w);
-                    a4 = load4(sa, kb + 4, p.nkb, p.vec_sa);
-                    w4 = load4(sw, kb + 4, p.nkb, p.vec_sw);
+                if (kb % S::kScaleRun == 0) {
+                    if (!(alive = wait_warp(&sfull[runs & 1], (runs >> 1) & 1, dead))) break;
+                    sc = scales + (runs & 1) * S::kScaleRun * S::kScaleRows;
                 }
-                const float s = s4.x;
-                s4 = make_float4(s4.y, s4.z, s4.w, 0.f);
+                // the columns of a thread lie in one 128-row block of W
+                const float* quad = sc + (kb % S::kScaleRun / 4) * 4 * S::kScaleRows + kb % 4;
+                const float s = quad[4 * r] * quad[4 * (128 + group * S::kCols / 128)];
                 if (!(alive = wait_warp(&tfull[buf], (it / S::kBufs) & 1, dead))) break;
                 tc_fence_after();
-                uint32_t d[2][S::kChunk];
-                tmem_ld(lanes + buf * BN, d[0]);
 #pragma unroll
-                for (int c = 0; c < S::kCols / S::kChunk; ++c) {
-                    tmem_wait_ld(d[c & 1]);
-                    if (c + 1 < S::kCols / S::kChunk) {
-                        tmem_ld(lanes + buf * BN + (c + 1) * S::kChunk, d[(c + 1) & 1]);
-                    } else {  // the accumulator is read
+                for (int c = 0; c < S::kCols; c += S::kChunk) {
+                    uint32_t d[S::kChunk];
+                    tmem_ld(lanes + buf * BN + c, d);
+                    tmem_wait_ld(d);
+                    if (c + S::kChunk == S::kCols) {  // the accumulator is read
                         tc_fence_before();
                         __syncwarp();
                         if (elect_one()) mbar_arrive_cluster(leader_tempty + buf * 8);
                     }
 #pragma unroll
-                    for (int j = 0; j < S::kChunk; ++j) {
-                        float& v = acc[c * S::kChunk + j];
-                        v = fmaf(__uint_as_float(d[c & 1][j]), s, v);
-                    }
+                    for (int j = 0; j < S::kChunk; ++j) acc[c + j] = fmaf(__uint_as_float(d[j]), s, acc[c + j]);
+                }
+                if ((kb + 1) % S::kScaleRun == 0 || kb + 1 == p.nkb) {
+                    __syncwarp();
+                    if (elect_one()) mbar_arrive(&sempty[runs & 1]);
+                    ++runs;
                 }
             }
             if (!alive || row >= p.m) continue;
