@@ -50,6 +50,17 @@ __device__ __forceinline__ bool mbar_poll(uint64_t* bar, uint32_t parity) {
         : "memory");
     return ok != 0;
 }
+// The same without suspending the thread (try_wait holds it for microseconds
+// when the phase is not complete).
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
 __device__ __forceinline__ bool wait_long(uint64_t* bar, uint32_t parity, volatile int* dead) {
     const long long t0 = clock64();
     while (!mbar_poll(bar, parity)) {
@@ -73,6 +84,21 @@ __device__ __forceinline__ bool wait_alive(uint64_t* bar, uint32_t parity, volat
 __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volatile int* dead) {
     return __all_sync(0xffffffffu, wait_alive(bar, parity, dead));
 }
+// Two barriers that one step waits for, asked one step ahead: the answer to a
+// poll takes about as long as issuing a block's matrix instructions, so the
+// polls for the next step go out before the instructions of this one, and the
+// step only waits where they came back empty.
+struct Ahead {
+    bool ok;
+    __device__ __forceinline__ void ask(uint64_t* a, uint32_t pa, uint64_t* b, uint32_t pb) {
+        const bool x = mbar_test(a, pa), y = mbar_test(b, pb);
+        ok = x && y;
+    }
+    __device__ __forceinline__ bool wait(uint64_t* a, uint32_t pa, uint64_t* b, uint32_t pb, volatile int* dead) {
+        if (__all_sync(0xffffffffu, ok)) return true;
+        return wait_warp(a, pa, dead) && wait_warp(b, pb, dead);
+    }
+};
 __device__ __forceinline__ bool elect_one() {
     uint32_t one;
     asm volatile(

@@ -285,7 +285,7 @@ struct GemmParams {
 
 constexpr int kMaxStages = 12;
 
-// Few rows of A (up to 128 per token tile): bound by reading W.  The weights
+// Few rows of A (up to 64): bound by reading W.  The weights
 // take the 128 lanes (MMA "A", 128 rows of W) and the TB tokens the columns,
 // so a tile costs the tensor cores little however few tokens there are, and
 // the K axis is split over the CTAs of a cluster, whose partial sums meet in
@@ -368,18 +368,21 @@ __global__ void __launch_bounds__(224) fp8_gemm_few_kernel(const __grid_constant
         if (it < nk) let_copies_land();
     } else if (warp == 1) {
         int st = 0, ph = 0, it = 0;
+        Ahead next;
+        next.ask(&full[0], 0, &tempty[0], 1);
         for (; it < nk; ++it) {
-            const int buf = it % S::kBufs;
-            if (!wait_warp(&full[st], ph, dead) || !wait_warp(&tempty[buf], ((it / S::kBufs) & 1) ^ 1, dead)) break;
+            const int buf = it % S::kBufs, used = st;
+            if (!next.wait(&full[st], ph, &tempty[buf], ((it / S::kBufs) & 1) ^ 1, dead)) break;
             tc_fence_after();
-            const uint32_t at = smem_u32(ring + st * S::kStageBytes);
+            if (++st == p.stages) st = 0, ph ^= 1;
+            next.ask(&full[st], ph, &tempty[(it + 1) % S::kBufs], (((it + 1) / S::kBufs) & 1) ^ 1);
+            const uint32_t at = smem_u32(ring + used * S::kStageBytes);
             if (elect_one()) {
                 mma_block(taddr + buf * TB, at, at + kTileBytes, p.idesc);
                 mma_commit(&tfull[buf]);
-                mma_commit(&empty[st]);
+                mma_commit(&empty[used]);
             }
             __syncwarp();
-            if (++st == p.stages) st = 0, ph ^= 1;
         }
         if (it < nk) let_copies_land();
     } else if (warp == 2) {
@@ -485,7 +488,7 @@ template <int BN>
 struct ManyShape {
     static constexpr int kRowsW = BN / 2;  // of W, in each CTA
     static constexpr int kStageBytes = kTileBytes + kRowsW * kBlockK;
-    static constexpr int kBufs = 512 / BN < 4 ? 512 / BN : 4;  // accumulators that take turns
+    static constexpr int kBufs = 512 / BN;  // accumulators that take turns
     static constexpr int kTmemCols = kBufs * BN;
     static constexpr int kPromotionWarps = 8;
     static constexpr int kThreads = 96 + kPromotionWarps * 32;
@@ -612,21 +615,24 @@ __global__ void __launch_bounds__(ManyShape<BN>::kThreads, 1) fp8_gemm_many_kern
             int st = 0, ph = 0;
             uint32_t it = 0;
             bool alive = true;
+            Ahead next;
+            next.ask(&full[0], 0, &tempty[0], 1);
             for (int64_t tile = pair; tile < tiles && alive; tile += pairs) {
-                for (int kb = 0; kb < p.nkb; ++kb, ++it) {
-                    const int buf = it % S::kBufs;
-                    // (the stage first: it is there long before the accumulator is free)
-                    alive = wait_warp(&full[st], ph, dead) && wait_warp(&tempty[buf], ((it / S::kBufs) & 1) ^ 1, dead);
+                for (int kb = 0; kb < p.nkb; ++kb) {
+                    const int buf = it % S::kBufs, used = st;
+                    alive = next.wait(&full[st], ph, &tempty[buf], ((it / S::kBufs) & 1) ^ 1, dead);
                     if (!alive) break;
                     tc_fence_after();
-                    const uint32_t at = smem_u32(ring + st * S::kStageBytes);
+                    if (++st == p.stages) st = 0, ph ^= 1;
+                    ++it;
+                    next.ask(&full[st], ph, &tempty[it % S::kBufs], ((it / S::kBufs) & 1) ^ 1);
+                    const uint32_t at = smem_u32(ring + used * S::kStageBytes);
                     if (elect_one()) {
                         mma_block_pair(taddr + buf * BN, at, at + kTileBytes, p.idesc);
                         mma_commit_pair(&tfull[buf]);
-                        mma_commit_pair(&empty[st]);
+                        mma_commit_pair(&empty[used]);
                     }
                     __syncwarp();
-                    if (++st == p.stages) st = 0, ph ^= 1;
                 }
             }
             if (!alive) let_copies_land();

@@ -550,79 +550,95 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
     const int u2a = S->cuts[1][blockIdx.x], u2b = S->cuts[1][blockIdx.x + 1];
 
     if (warp == 0) {  // ---------------------------------------------- weights
-        if (lane == 0) {
-            int st = 0, ph = 0;
-            bool alive = true;
-            if (u1a < u1b) {
-                int kb = u1a % nkb1, ti = u1a / nkb1 % p.tiles_i, a = u1a / nkb1 / p.tiles_i, e = R->active[a];
-                for (int u = u1a; u < u1b && alive; ++u) {
+        int st = 0, ph = 0;
+        bool alive = true;
+        if (u1a < u1b) {
+            int kb = u1a % nkb1, ti = u1a / nkb1 % p.tiles_i, a = u1a / nkb1 / p.tiles_i, e = R->active[a];
+            for (int u = u1a; u < u1b && alive; ++u) {
 #pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        if (!(alive = wait_alive(&S->empty[st], ph ^ 1, dead))) break;
+                for (int half = 0; half < 2; ++half) {
+                    if (!(alive = wait_warp(&S->empty[st], ph ^ 1, dead))) break;
+                    if (elect_one()) {
                         mbar_expect_tx(&S->full[st], kTileBytes);
                         tma_load_3d(ring + st * p.stage_bytes, &map_w13, &S->full[st], kb * kBlockK, ti * 128, 2 * e + half);
-                        if (++st == p.stages) st = 0, ph ^= 1;
                     }
-                    if (++kb == nkb1) {
-                        kb = 0;
-                        if (++ti == p.tiles_i && ++a < n_act) e = R->active[a];
-                        if (ti == p.tiles_i) ti = 0;
-                    }
+                    __syncwarp();
+                    if (++st == p.stages) st = 0, ph ^= 1;
+                }
+                if (++kb == nkb1) {
+                    kb = 0;
+                    if (++ti == p.tiles_i && ++a < n_act) e = R->active[a];
+                    if (ti == p.tiles_i) ti = 0;
                 }
             }
-            if (u2a < u2b) {
-                int kb = u2a % nkb2, a = u2a / nkb2 % n_act, rt = u2a / nkb2 / n_act;
-                for (int u = u2a; u < u2b && alive; ++u) {
-                    if (!(alive = wait_alive(&S->empty[st], ph ^ 1, dead))) break;
+        }
+        if (u2a < u2b) {
+            int kb = u2a % nkb2, a = u2a / nkb2 % n_act, rt = u2a / nkb2 / n_act, e = R->active[a];
+            for (int u = u2a; u < u2b && alive; ++u) {
+                if (!(alive = wait_warp(&S->empty[st], ph ^ 1, dead))) break;
+                if (elect_one()) {
                     mbar_expect_tx(&S->full[st], kTileBytes);
-                    tma_load_3d(ring + st * p.stage_bytes, &map_w2, &S->full[st], kb * kBlockK, rt * 128, R->active[a]);
-                    if (++st == p.stages) st = 0, ph ^= 1;
-                    if (++kb == nkb2) {
-                        kb = 0;
-                        if (++a == n_act) a = 0, ++rt;
-                    }
+                    tma_load_3d(ring + st * p.stage_bytes, &map_w2, &S->full[st], kb * kBlockK, rt * 128, e);
                 }
-            }
-            if (!alive) let_copies_land();
-        }
-    } else if (warp == 1) {  // ---------------------------- matrix instructions
-        if (lane == 0) {
-            const uint32_t idesc = instr_desc(0, 0, 128, cols);
-            int st = 0, ph = 0;
-            uint32_t it = 0;
-            bool alive = true;
-            for (int u = u1a; u < u1b && alive; ++u, ++it) {
-                const int buf = it & (bufs - 1);
-                alive = wait_alive(&S->tempty[buf], ((it >> bufs_log) & 1) ^ 1, dead);
-                uint32_t b = 0, first = 0;
-#pragma unroll
-                for (int half = 0; half < 2 && alive; ++half) {
-                    if (!(alive = wait_alive(&S->full[st], ph, dead))) break;
-                    tc_fence_after();
-                    const uint32_t at = smem_u32(ring + st * p.stage_bytes);
-                    if (half == 0) b = at + kTileBytes, first = st;  // the up tile shares the gate tile's digits
-                    mma_block(taddr + (buf * 2 + half) * cols, at, b, idesc);
-                    if (half == 1) {
-                        mma_commit(&S->empty[first]);
-                        mma_commit(&S->empty[st]);
-                        mma_commit(&S->tfull[buf]);
-                    }
-                    if (++st == p.stages) st = 0, ph ^= 1;
-                }
-            }
-            for (int u = u2a; u < u2b && alive; ++u, ++it) {
-                const int buf = it & (bufs - 1);
-                alive = wait_alive(&S->tempty[buf], ((it >> bufs_log) & 1) ^ 1, dead) && wait_alive(&S->full[st], ph, dead);
-                if (!alive) break;
-                tc_fence_after();
-                const uint32_t at = smem_u32(ring + st * p.stage_bytes);
-                mma_block(taddr + buf * 2 * cols, at, at + kTileBytes, idesc);
-                mma_commit(&S->empty[st]);
-                mma_commit(&S->tfull[buf]);
+                __syncwarp();
                 if (++st == p.stages) st = 0, ph ^= 1;
+                if (++kb == nkb2) {
+                    kb = 0;
+                    if (++a == n_act) a = 0, ++rt;
+                    e = R->active[a];
+                }
             }
-            if (!alive) let_copies_land();
         }
+        if (!alive) let_copies_land();
+    } else if (warp == 1) {  // ---------------------------- matrix instructions
+        const uint32_t idesc = instr_desc(0, 0, 128, cols);
+        int st = 0, ph = 0;
+        uint32_t it = 0;
+        bool alive = true;
+        Ahead next;
+        next.ask(&S->full[0], 0, &S->tempty[0], 1);
+        for (int u = u1a; u < u1b; ++u) {
+            const int buf = it & (bufs - 1), gate = st;
+            alive = next.wait(&S->full[st], ph, &S->tempty[buf], ((it >> bufs_log) & 1) ^ 1, dead);
+            if (!alive) break;
+            if (++st == p.stages) st = 0, ph ^= 1;
+            const int up = st;
+            const bool up_there = mbar_test(&S->full[st], ph);
+            tc_fence_after();
+            const uint32_t at = smem_u32(ring + gate * p.stage_bytes), digits = at + kTileBytes;
+            if (elect_one()) mma_block(taddr + buf * 2 * cols, at, digits, idesc);
+            __syncwarp();
+            if (!__all_sync(0xffffffffu, up_there)) alive = wait_warp(&S->full[st], ph, dead);
+            if (!alive) break;
+            tc_fence_after();
+            if (++st == p.stages) st = 0, ph ^= 1;
+            ++it;
+            next.ask(&S->full[st], ph, &S->tempty[it & (bufs - 1)], ((it >> bufs_log) & 1) ^ 1);
+            if (elect_one()) {  // the up tile shares the gate tile's digits
+                mma_block(taddr + (buf * 2 + 1) * cols, smem_u32(ring + up * p.stage_bytes), digits, idesc);
+                mma_commit(&S->tfull[buf]);
+                mma_commit(&S->empty[gate]);
+                mma_commit(&S->empty[up]);
+            }
+            __syncwarp();
+        }
+        for (int u = u2a; u < u2b && alive; ++u) {
+            const int buf = it & (bufs - 1), used = st;
+            alive = next.wait(&S->full[st], ph, &S->tempty[buf], ((it >> bufs_log) & 1) ^ 1, dead);
+            if (!alive) break;
+            tc_fence_after();
+            if (++st == p.stages) st = 0, ph ^= 1;
+            ++it;
+            next.ask(&S->full[st], ph, &S->tempty[it & (bufs - 1)], ((it >> bufs_log) & 1) ^ 1);
+            const uint32_t at = smem_u32(ring + used * p.stage_bytes);
+            if (elect_one()) {
+                mma_block(taddr + buf * 2 * cols, at, at + kTileBytes, idesc);
+                mma_commit(&S->tfull[buf]);
+                mma_commit(&S->empty[used]);
+            }
+            __syncwarp();
+        }
+        if (!alive) let_copies_land();
     } else if (warp == 2) {  // ------------------------ digits and their scales
         int st = 0, ph = 0;
         uint32_t it = 0;

@@ -118,7 +118,9 @@ sqz_status launch_many(const CUtensorMap& mw, const CUtensorMap& ma, GemmParams 
     return SQZ_OK;
 }
 
-constexpr int kFewRows = 128;  // up to here the few-row kernel, above it the many-row kernel
+// Up to here the few-row kernel, above it the many-row kernel (4096 x 4096: 64
+// rows 10 us, 128 rows 34 us against 15).
+constexpr int kFewRows = 64;
 
 sqz_status check_matrix(const sqz_fp8_matrix* x, const char* name, int64_t rows, int32_t k) {
     if (!x) return host_fail(SQZ_ERR_INVALID_ARG, "%s is NULL", name);
@@ -252,8 +254,7 @@ extern "C" SQZ_API sqz_status sqz_fp8_gemm(const sqz_fp8_matrix* a, const sqz_fp
         switch (tb) {
             case 16: return launch_few<16>(mw, ma, p, splits, stages, d, s);
             case 32: return launch_few<32>(mw, ma, p, splits, stages, d, s);
-            case 64: return launch_few<64>(mw, ma, p, splits, stages, d, s);
-            default: return launch_few<128>(mw, ma, p, splits, stages, d, s);
+            default: return launch_few<64>(mw, ma, p, splits, stages, d, s);
         }
     }
     // The widest tile costs least per output; narrower ones when they need
