@@ -89,14 +89,16 @@ __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volati
 // polls for the next step go out before the instructions of this one, and the
 // step only waits where they came back empty.
 struct Ahead {
-    bool ok;
+    bool a_there, b_there;
     __device__ __forceinline__ void ask(uint64_t* a, uint32_t pa, uint64_t* b, uint32_t pb) {
-        const bool x = mbar_test(a, pa), y = mbar_test(b, pb);
-        ok = x && y;
+        a_there = mbar_test(a, pa);
+        b_there = mbar_test(b, pb);
     }
     __device__ __forceinline__ bool wait(uint64_t* a, uint32_t pa, uint64_t* b, uint32_t pb, volatile int* dead) {
-        if (__all_sync(0xffffffffu, ok)) return true;
-        return wait_warp(a, pa, dead) && wait_warp(b, pb, dead);
+        bool ok = true;
+        if (!__all_sync(0xffffffffu, a_there)) ok = wait_warp(a, pa, dead);
+        if (ok && !__all_sync(0xffffffffu, b_there)) ok = wait_warp(b, pb, dead);
+        return ok;
     }
 };
 __device__ __forceinline__ bool elect_one() {
@@ -104,6 +106,16 @@ __device__ __forceinline__ bool elect_one() {
     asm volatile(
         "{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(one));
     return one != 0;
+}
+
+// Registers of a warpgroup's threads, up or down to N (all four warps).
+template <int N>
+__device__ __forceinline__ void regs_up() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_down() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
 // After a wait gave up: time (100 ms) for the thread's own copies and matrix
@@ -130,13 +142,13 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, u
 __device__ __forceinline__ void tma_prefetch_map(const CUtensorMap* map) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }
-// Asynchronous 4-byte copy to shared memory; `valid` false writes zero.  The
-// thread's arrival on `bar` is posted when its copies so far have landed (it
-// counts as one of the barrier's expected arrivals).
-__device__ __forceinline__ void cp_async4(void* dst, const void* src, bool valid) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(valid ? 4 : 0)
-                 : "memory");
+// Asynchronous 4-byte copy to shared memory.  (Lanes that have nothing to copy
+// stay out: lanes copying from one address, even zero bytes, go one by one.)
+__device__ __forceinline__ void cp_async4(void* dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
 }
+// The thread's arrival on `bar`, posted when its copies so far have landed (it
+// counts as one of the barrier's expected arrivals).
 __device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }

@@ -393,11 +393,9 @@ __global__ void __launch_bounds__(224) fp8_gemm_few_kernel(const __grid_constant
             float* dst = scales + st * S::kScaleFloats;
             const int kb = kb0 + it;
 #pragma unroll
-            for (int t = lane; t < TB; t += 32) {
-                const bool ok = tok0 + t < p.m;
-                cp_async4(dst + t, p.sa + (ok ? (int64_t)(tok0 + t) * p.ld_sa + kb : 0), ok);
-            }
-            if (lane == 0) cp_async4(dst + TB, sw + kb, true);
+            for (int t = lane; t < TB; t += 32)  // (a column of no token is never stored: any scale does)
+                if (tok0 + t < p.m) cp_async4(dst + t, p.sa + (int64_t)(tok0 + t) * p.ld_sa + kb);
+            if (lane == 0) cp_async4(dst + TB, sw + kb);
             cp_async_arrive(&full[st]);
             if (++st == p.stages) st = 0, ph ^= 1;
         }
@@ -537,7 +535,7 @@ __device__ __forceinline__ void copy_scales(float* dst, const float* src, int n,
     if (vec && n == 4) {
         tc::cp_async16(dst, src);
     } else {
-        for (int i = 0; i < n; ++i) cp_async4(dst + i, src + i, true);
+        for (int i = 0; i < n; ++i) cp_async4(dst + i, src + i);
     }
 }
 
@@ -590,13 +588,15 @@ __global__ void __launch_bounds__(ManyShape<BN>::kThreads, 1) fp8_gemm_many_kern
         const uint32_t leader_full = cluster_addr(full, 0);
         for (int64_t tile = pair; tile < tiles && alive; tile += pairs) {
             const int tn = (int)(tile / p.tiles_m), tm = (int)(tile - (int64_t)tn * p.tiles_m);
+            // a CTA whose rows all lie past the last one multiplies the first ones
+            const int row0 = tm * 256 + rank * 128 < p.m ? tm * 256 + rank * 128 : 0;
             for (int kb = 0; kb < p.nkb; ++kb) {
                 if (!(alive = wait_warp(&empty[st], ph ^ 1, dead))) break;
                 const uint32_t bar = leader_full + st * 8;
                 uint8_t* at = ring + st * S::kStageBytes;
                 if (elect_one()) {
                     if (rank == 0) mbar_expect_tx(&full[st], 2 * S::kStageBytes);
-                    tma_load_2d_pair(at, &map_a, bar, kb * kBlockK, tm * 256 + rank * 128);
+                    tma_load_2d_pair(at, &map_a, bar, kb * kBlockK, row0);
                     tma_load_2d_pair(at + kTileBytes, &map_w, bar, kb * kBlockK, tn * BN + rank * S::kRowsW);
                 }
                 __syncwarp();
@@ -646,15 +646,15 @@ __global__ void __launch_bounds__(ManyShape<BN>::kThreads, 1) fp8_gemm_many_kern
             for (int k0 = 0; k0 < p.nkb; k0 += S::kScaleRun, ++runs) {
                 if (!(alive = wait_warp(&sempty[runs & 1], ((runs >> 1) & 1) ^ 1, dead))) break;
                 float* dst = scales + (runs & 1) * S::kScaleRun * S::kScaleRows;
-                const int wb = min(tn * BN / 128 + lane, w_blocks - 1);
+                const int wb = tn * BN / 128 + lane;
                 for (int k = k0; k < min(k0 + S::kScaleRun, p.nkb); k += 4, dst += 4 * S::kScaleRows) {
                     const int n = min(4, p.nkb - k);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int64_t row = min(tm * 256 + rank * 128 + i * 32 + lane, p.m - 1);
-                        copy_scales(dst + 4 * (i * 32 + lane), p.sa + row * p.ld_sa + k, n, p.vec_sa);
+                    for (int i = 0; i < 4; ++i) {  // (what belongs to no row is never stored: any scale does)
+                        const int64_t row = tm * 256 + rank * 128 + i * 32 + lane;
+                        if (row < p.m) copy_scales(dst + 4 * (i * 32 + lane), p.sa + row * p.ld_sa + k, n, p.vec_sa);
                     }
-                    if (lane < (BN + 127) / 128)
+                    if (lane < (BN + 127) / 128 && wb < w_blocks)
                         copy_scales(dst + 4 * (128 + lane), p.sw + wb * p.ld_sw + k, n, p.vec_sw);
                 }
                 cp_async_arrive(&sfull[runs & 1]);

@@ -660,8 +660,8 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
                 if (lane < n)
                     tma_load_2d(ring + st * p.stage_bytes + kTileBytes + lane * kDigits * kBlockK, &map_x, &S->full[st],
                                 kb * kBlockK, t * kDigits);
-                if (lane < n) cp_async4(&S->scale[slot][lane], sx + kb, true);
-                if (lane < 2) cp_async4(&S->scale[slot][kMaxTokens + lane], sw + kb, true);
+                if (lane < n) cp_async4(&S->scale[slot][lane], sx + kb);
+                if (lane < 2) cp_async4(&S->scale[slot][kMaxTokens + lane], sw + kb);
                 cp_async_arrive(&S->sfull[slot]);
                 if (++st == p.stages) st = 0, ph ^= 1;
                 // the up tile's stage brings no digits of its own
@@ -694,8 +694,8 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
                 if (lane < n)
                     tma_load_2d(ring + st * p.stage_bytes + kTileBytes + lane * kDigits * kBlockK, &map_h, &S->full[st],
                                 kb * kBlockK, row * kDigits);
-                if (lane < n) cp_async4(&S->scale[slot][lane], sh + kb, true);
-                if (lane == 0) cp_async4(&S->scale[slot][kMaxTokens], sw + kb, true);
+                if (lane < n) cp_async4(&S->scale[slot][lane], sh + kb);
+                if (lane == 0) cp_async4(&S->scale[slot][kMaxTokens], sw + kb);
                 cp_async_arrive(&S->sfull[slot]);
                 if (++st == p.stages) st = 0, ph ^= 1;
             }
