@@ -279,7 +279,6 @@ struct GemmParams {
     uint32_t idesc;
     int stages;
     int tiles_m, tiles_n;  // many-row kernel
-    int vec_sa, vec_sw;    // rows of scales are 16-byte aligned
     int out_align;         // alignment of y's rows in bytes: 32, 16 or less
 };
 
@@ -487,10 +486,11 @@ struct ManyShape {
     static constexpr int kRowsW = BN / 2;  // of W, in each CTA
     static constexpr int kStageBytes = kTileBytes + kRowsW * kBlockK;
     static constexpr int kBufs = 512 / BN;  // accumulators that take turns
-    static constexpr int kTmemCols = kBufs * BN;
+    static constexpr int kTmemCols = kBufs * BN > 256 ? 512 : 256;  // (allocated in powers of two)
     static constexpr int kPromotionWarps = 8;
     static constexpr int kThreads = 96 + kPromotionWarps * 32;
     static constexpr int kCols = BN / 2;   // columns of a thread
+    static constexpr bool kOneBlock = 256 % BN == 0;  // ... lie in one block of 128 rows of W (else in two)
     static constexpr int kChunk = 16;      // columns of a load from tensor memory
     // scales of kScaleRun blocks of K at a time, [four blocks][128 rows of A, 2 for W][4]
     static constexpr int kScaleRun = 16;
@@ -525,17 +525,6 @@ __device__ __forceinline__ void store_row(const GemmParams& p, int64_t at, const
             st_global_32b(y + j, pack2u(w[0], w[1]), pack2u(w[2], w[3]), pack2u(w[4], w[5]), pack2u(w[6], w[7]),
                           p.out_align);
         }
-    }
-}
-
-// Up to four consecutive scales to shared memory, asynchronously (in one copy
-// where the row is 16-byte aligned and four are left: a copy costs a line of L1
-// per lane whatever its width).
-__device__ __forceinline__ void copy_scales(float* dst, const float* src, int n, bool vec) {
-    if (vec && n == 4) {
-        tc::cp_async16(dst, src);
-    } else {
-        for (int i = 0; i < n; ++i) cp_async4(dst + i, src + i);
     }
 }
 
@@ -646,16 +635,16 @@ __global__ void __launch_bounds__(ManyShape<BN>::kThreads, 1) fp8_gemm_many_kern
             for (int k0 = 0; k0 < p.nkb; k0 += S::kScaleRun, ++runs) {
                 if (!(alive = wait_warp(&sempty[runs & 1], ((runs >> 1) & 1) ^ 1, dead))) break;
                 float* dst = scales + (runs & 1) * S::kScaleRun * S::kScaleRows;
-                const int wb = tn * BN / 128 + lane;
-                for (int k = k0; k < min(k0 + S::kScaleRun, p.nkb); k += 4, dst += 4 * S::kScaleRows) {
-                    const int n = min(4, p.nkb - k);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {  // (what belongs to no row is never stored: any scale does)
-                        const int64_t row = tm * 256 + rank * 128 + i * 32 + lane;
-                        if (row < p.m) copy_scales(dst + 4 * (i * 32 + lane), p.sa + row * p.ld_sa + k, n, p.vec_sa);
-                    }
-                    if (lane < (BN + 127) / 128 && wb < w_blocks)
-                        copy_scales(dst + 4 * (128 + lane), p.sw + wb * p.ld_sw + k, n, p.vec_sw);
+                // A half-warp copies a row's run of consecutive scales: few lines of
+                // L1 a copy, whatever the pitch.  (What belongs to no row is never
+                // stored: any scale does.)
+                const int k = k0 + (lane & 15), at = (lane & 15) / 4 * 4 * S::kScaleRows + (lane & 3);
+                if (k < p.nkb) {
+                    const int first = tm * 256 + rank * 128, rows = min(128, p.m - first);
+                    for (int i = lane / 16; i < rows; i += 2)
+                        cp_async4(dst + at + 4 * i, p.sa + (int64_t)(first + i) * p.ld_sa + k);
+                    const int wb = tn * BN / 128 + lane / 16;
+                    if (wb < w_blocks) cp_async4(dst + at + 4 * (128 + lane / 16), p.sw + wb * p.ld_sw + k);
                 }
                 cp_async_arrive(&sfull[runs & 1]);
             }
@@ -671,6 +660,9 @@ __global__ void __launch_bounds__(ManyShape<BN>::kThreads, 1) fp8_gemm_many_kern
             const int tn = (int)(tile / p.tiles_m), tm = (int)(tile - (int64_t)tn * p.tiles_m);
             const int64_t row = (int64_t)tm * 256 + rank * 128 + r;
             const int col0 = tn * BN + group * S::kCols;
+            // the block of W that the thread's first column lies in (of the
+            // tile's), and its first column of the next one
+            const int block = col0 / 128 - tn * BN / 128, split = (col0 / 128 + 1) * 128 - col0;
             float acc[S::kCols];
 #pragma unroll
             for (int j = 0; j < S::kCols; ++j) acc[j] = 0.f;
@@ -681,9 +673,9 @@ __global__ void __launch_bounds__(ManyShape<BN>::kThreads, 1) fp8_gemm_many_kern
                     if (!(alive = wait_warp(&sfull[runs & 1], (runs >> 1) & 1, dead))) break;
                     sc = scales + (runs & 1) * S::kScaleRun * S::kScaleRows;
                 }
-                // the columns of a thread lie in one 128-row block of W
                 const float* quad = sc + (kb % S::kScaleRun / 4) * 4 * S::kScaleRows + kb % 4;
-                const float s = quad[4 * r] * quad[4 * (128 + group * S::kCols / 128)];
+                const float s0 = quad[4 * r] * quad[4 * (128 + block)];
+                const float s1 = S::kOneBlock ? s0 : quad[4 * r] * quad[4 * (128 + 1)];
                 if (!(alive = wait_warp(&tfull[buf], (it / S::kBufs) & 1, dead))) break;
                 tc_fence_after();
 #pragma unroll
@@ -697,7 +689,8 @@ __global__ void __launch_bounds__(ManyShape<BN>::kThreads, 1) fp8_gemm_many_kern
                         if (elect_one()) mbar_arrive_cluster(leader_tempty + buf * 8);
                     }
 #pragma unroll
-                    for (int j = 0; j < S::kChunk; ++j) acc[c + j] = fmaf(__uint_as_float(d[j]), s, acc[c + j]);
+                    for (int j = 0; j < S::kChunk; ++j)
+                        acc[c + j] = fmaf(__uint_as_float(d[j]), S::kOneBlock || c < split ? s0 : s1, acc[c + j]);
                 }
                 if ((kb + 1) % S::kScaleRun == 0 || kb + 1 == p.nkb) {
                     __syncwarp();

@@ -229,8 +229,6 @@ extern "C" SQZ_API sqz_status sqz_fp8_gemm(const sqz_fp8_matrix* a, const sqz_fp
     p.n = n;
     p.nkb = (k + 127) / 128;
     p.out_type = y_type;
-    p.vec_sa = reinterpret_cast<uintptr_t>(p.sa) % 16 == 0 && p.ld_sa % 4 == 0;
-    p.vec_sw = reinterpret_cast<uintptr_t>(p.sw) % 16 == 0 && p.ld_sw % 4 == 0;
     p.out_align = 32;
     while (p.out_align > 2 && (reinterpret_cast<uintptr_t>(y) % p.out_align || ldy * out_bytes % p.out_align))
         p.out_align /= 2;
@@ -257,20 +255,24 @@ extern "C" SQZ_API sqz_status sqz_fp8_gemm(const sqz_fp8_matrix* a, const sqz_fp
             default: return launch_few<64>(mw, ma, p, splits, stages, d, s);
         }
     }
-    // The widest tile costs least per output; narrower ones when they need
-    // fewer rounds of the pairs of SMs (weights: measured time of a tile's block of K).
+    // The width of the tiles: the least rounds of the pairs of SMs times a
+    // tile's time for a block of K, which measured 0.29, 0.35 and 0.56 us for
+    // 64, 128 and 256 columns: about proportional to 120 + width.
     const int64_t tm = (m + 255) / 256, pairs = d.sms / 2;
-    const auto rounds = [&](int bn, double weight) {
-        const int64_t tiles = tm * (((int64_t)n + bn - 1) / bn);
-        return (double)((tiles + pairs - 1) / pairs) * weight;
-    };
-    const double c256 = rounds(256, 1.0), c128 = rounds(128, 0.6), c64 = rounds(64, 0.45);
-    const int bn = c256 <= c128 && c256 <= c64 ? 256 : c128 <= c64 ? 128 : 64;
+    int bn = 256;
+    int64_t least = INT64_MAX;
+    for (int width : {256, 192, 160, 128, 64}) {
+        const int64_t tiles = tm * (((int64_t)n + width - 1) / width);
+        const int64_t cost = (tiles + pairs - 1) / pairs * (120 + width);
+        if (cost < least) least = cost, bn = width;
+    }
     if ((st = tile_map(&mw, w->q, k, n, w->ld, bn / 2)) != SQZ_OK) return st;
     if ((st = tile_map(&ma, a->q, k, m, a->ld, 128)) != SQZ_OK) return st;
     p.idesc = instr_desc(a->format, w->format, 256, bn);
     switch (bn) {
         case 256: return launch_many<256>(mw, ma, p, d, s);
+        case 192: return launch_many<192>(mw, ma, p, d, s);
+        case 160: return launch_many<160>(mw, ma, p, d, s);
         case 128: return launch_many<128>(mw, ma, p, d, s);
         default: return launch_many<64>(mw, ma, p, d, s);
     }

@@ -149,6 +149,8 @@ SIZES = [
     (1, 1, 1), (1, 8, 16), (1, 128, 128), (1, 4096, 4096), (2, 300, 1000), (16, 129, 513), (17, 128, 2048),
     (33, 1000, 300), (64, 640, 1152), (65, 200, 4100), (128, 257, 129), (129, 300, 130), (200, 64, 640),
     (257, 1111, 272), (500, 2050, 1000), (1000, 2048, 128), (300, 40, 5000),
+    # every tile width: 160, 192 and 256 columns, the last ones partial, W's blocks ending inside a tile
+    (300, 5000, 300), (290, 6900, 300), (70, 11000, 390), (200, 19000, 130), (256, 18000, 130),
 ]
 
 
