@@ -305,7 +305,7 @@ __device__ __forceinline__ void route_token(const Params& p, Routing* R, uint32_
 #pragma unroll 2
     for (int e = lane; e < p.experts; e += 32) sum += expf(key_logit(keys[e]) - top);
     sum = warp_sum(sum);
-    float mine = 0.f, chosen_sum = 0.f;
+    uint32_t mine = 0;  // lane j: the j-th choice's key
     int mine_id = 0;
 #pragma unroll 1
     for (int j = 0; j < p.top_k; ++j) {
@@ -318,12 +318,11 @@ __device__ __forceinline__ void route_token(const Params& p, Routing* R, uint32_
         const uint32_t high = __reduce_max_sync(0xffffffffu, k);
         const uint32_t e = __reduce_min_sync(0xffffffffu, k == high ? at : 0xffffffffu);
         if (e == at) keys[e] = 0;
-        const float w = expf(key_logit(high) - top) / sum;
-        chosen_sum += w;
-        if (lane == j) mine = w, mine_id = (int)e;
+        if (lane == j) mine = high, mine_id = (int)e;
     }
+    float w = lane < p.top_k ? expf(key_logit(mine) - top) / sum : 0.f;
+    if (p.renormalize) w = w / warp_sum(w);
     if (lane < p.top_k) {
-        const float w = p.renormalize ? mine / chosen_sum : mine;
         R->id[t * p.top_k + lane] = (uint16_t)mine_id;
         R->weight[t * p.top_k + lane] = w;
         atomicOr(&R->mask[mine_id], 1u << t);
@@ -381,12 +380,13 @@ __device__ __forceinline__ int owner(const int* cuts, int u) {
 // Sums of a tile's pieces in CTA order: four consecutive floats at `at` and
 // four more 1024 floats further on (256 threads cover a run of 1024).  Pieces
 // lie [CTA][at the tile's start: 1, later: 0][size floats], `size` of them in
-// use.  The loads of up to eight pieces are in flight together.
+// use; this CTA's own is passed in.  The loads of up to eight pieces are in
+// flight together.
 struct Joined {
     float4 v[2];
 };
-__device__ __forceinline__ Joined join4(const float* pieces, int64_t size, int at, const int* cuts, int c0, int c1,
-                                        int first, int used) {
+__device__ __forceinline__ Joined join4(const Joined& own, const float* pieces, int64_t size, int at, const int* cuts,
+                                        int c0, int c1, int first, int used) {
     Joined s;
     s.v[0] = s.v[1] = make_float4(0.f, 0.f, 0.f, 0.f);
     const bool two = at + 1024 < used;
@@ -399,8 +399,12 @@ __device__ __forceinline__ Joined join4(const float* pieces, int64_t size, int a
             const float4* src =
                 reinterpret_cast<const float4*>(pieces + (c * 2 + (from > first ? 0 : 1)) * size + at);
             w[0][j] = w[1][j] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (on) w[0][j] = __ldcg(src);
-            if (on && two) w[1][j] = __ldcg(src + 256);
+            if (on && c == blockIdx.x) {
+                w[0][j] = own.v[0], w[1][j] = own.v[1];
+            } else if (on) {
+                w[0][j] = __ldcg(src);
+                if (two) w[1][j] = __ldcg(src + 256);
+            }
         }
 #pragma unroll
         for (int k = 0; k < 2; ++k)
@@ -728,6 +732,20 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
             }
             ++it;
         };
+        // Whether the other CTAs' pieces of a tile are all there: then this CTA
+        // completes it, and its own piece need not leave the SM.  (Asked for the
+        // tile a CTA ends inside of: the next CTA starts with the rest of it.)
+        const auto others_done = [&](int* counter, int len, int whole) {
+            bar_promotion();
+            if (first_thread) {
+                int done;
+                asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(done) : "l"(counter) : "memory");
+                S->last = done + len == whole;
+                if (S->last) *counter = 0;  // for the next call
+            }
+            bar_promotion();
+            return S->last != 0;
+        };
         // Adds `len` of a tile's `whole` units to its counter once the pieces
         // of all 256 threads are written; true for the CTA that completes it.
         const auto is_last = [&](int* counter, int len, int whole) {
@@ -765,17 +783,24 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
                 if (i < n) own[i * 256] = acc[i / 4][i % 4];
             bool mine = len == nkb1;
             if (!mine) {  // a piece: at the tile's start (then the CTA's last tile) or not (then its first)
-                float* dst = p.part1 + ((int64_t)(blockIdx.x * 2 + (k0 > 0 ? 0 : 1)) * p.tokens) * 256 + group * 128 + r;
+                const int slot = k0 > 0 ? 0 : 1;
+                mine = slot == 1 && others_done(p.cnt1 + tile, len, nkb1);
+                if (!mine) {
+                    float* dst = p.part1 + (int64_t)(blockIdx.x * 2 + slot) * p.tokens * 256 + group * 128 + r;
 #pragma unroll 2
-                for (int i = 0; i < n; ++i) __stcg(dst + i * 256, own[i * 256]);
-                if ((mine = is_last(p.cnt1 + tile, len, nkb1))) {
-                    const int first = tile * nkb1, c0 = owner(S->cuts[0], first);
+                    for (int i = 0; i < n; ++i) __stcg(dst + i * 256, own[i * 256]);
+                    mine = is_last(p.cnt1 + tile, len, nkb1);
+                }
+                if (mine) {
+                    const int first = tile * nkb1, used = n * 256, c0 = owner(S->cuts[0], first);
                     const int c1 = owner(S->cuts[0], first + nkb1 - 1);
-                    for (int i = pt * 4; i < n * 256; i += 2048) {
-                        const Joined s =
-                            join4(p.part1, (int64_t)p.tokens * 256, i, S->cuts[0], c0, c1, first, n * 256);
+                    for (int i = pt * 4; i < used; i += 2048) {
+                        Joined s;
+                        s.v[0] = *reinterpret_cast<const float4*>(sums + i);
+                        if (i + 1024 < used) s.v[1] = *reinterpret_cast<const float4*>(sums + i + 1024);
+                        s = join4(s, p.part1, (int64_t)p.tokens * 256, i, S->cuts[0], c0, c1, first, used);
                         *reinterpret_cast<float4*>(sums + i) = s.v[0];
-                        if (i + 1024 < n * 256) *reinterpret_cast<float4*>(sums + i + 1024) = s.v[1];
+                        if (i + 1024 < used) *reinterpret_cast<float4*>(sums + i + 1024) = s.v[1];
                     }
                 }
             }
@@ -842,24 +867,33 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
             }
             bar_promotion();
             // the two groups' sums meet; a thread takes four rows of a token
-            const bool whole = len == per;
-            float* dst = p.part2 + ((int64_t)(blockIdx.x * 2 + (k0 > 0 ? 0 : 1)) * p.tokens) * 128;
-            for (int i = pt * 4; i < p.tokens * 128; i += 1024) {
+            const int used = p.tokens * 128, slot = k0 > 0 ? 0 : 1;
+            const auto met = [&](int i) {
                 float4 v = *reinterpret_cast<const float4*>(sums + i);
-                const float4 w = *reinterpret_cast<const float4*>(sums + p.tokens * 128 + i);
+                const float4 w = *reinterpret_cast<const float4*>(sums + used + i);
                 v.x += w.x, v.y += w.y, v.z += w.z, v.w += w.w;
-                if (whole)
-                    store_y<BF16>(p, i / 128, rt * 128 + i % 128, v);
-                else
-                    __stcg(reinterpret_cast<float4*>(dst + i), v);
-            }
-            if (!whole && is_last(p.cnt2 + rt, len, per)) {
-                const int first = rt * per, used = p.tokens * 128, c0 = owner(S->cuts[1], first);
-                const int c1 = owner(S->cuts[1], first + per - 1);
-                for (int i = pt * 4; i < used; i += 2048) {
-                    const Joined s = join4(p.part2, used, i, S->cuts[1], c0, c1, first, used);
-                    store_y<BF16>(p, i / 128, rt * 128 + i % 128, s.v[0]);
-                    if (i + 1024 < used) store_y<BF16>(p, i / 128 + 8, rt * 128 + i % 128, s.v[1]);
+                return v;
+            };
+            if (len == per) {
+                for (int i = pt * 4; i < used; i += 1024) store_y<BF16>(p, i / 128, rt * 128 + i % 128, met(i));
+            } else {
+                bool mine = slot == 1 && others_done(p.cnt2 + rt, len, per);
+                if (!mine) {
+                    float* dst = p.part2 + (int64_t)(blockIdx.x * 2 + slot) * used;
+                    for (int i = pt * 4; i < used; i += 1024) __stcg(reinterpret_cast<float4*>(dst + i), met(i));
+                    mine = is_last(p.cnt2 + rt, len, per);
+                }
+                if (mine) {
+                    const int first = rt * per, c0 = owner(S->cuts[1], first);
+                    const int c1 = owner(S->cuts[1], first + per - 1);
+                    for (int i = pt * 4; i < used; i += 2048) {
+                        Joined s;
+                        s.v[0] = met(i);
+                        if (i + 1024 < used) s.v[1] = met(i + 1024);
+                        s = join4(s, p.part2, used, i, S->cuts[1], c0, c1, first, used);
+                        store_y<BF16>(p, i / 128, rt * 128 + i % 128, s.v[0]);
+                        if (i + 1024 < used) store_y<BF16>(p, i / 128 + 8, rt * 128 + i % 128, s.v[1]);
+                    }
                 }
             }
             bar_promotion();  // `sums` is read
