@@ -480,6 +480,12 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
         for (int c = threadIdx.x * 64; c < p.hidden; c += kThreads * 64)
             asm volatile("prefetch.global.L2 [%0];" ::"l"(p.router + blockIdx.x / groups * p.ld_router + c));
     if (warp == 1) tmem_alloc(&S->taddr, 512);
+    if (warp == 2 && lane == 0) {
+        tma_prefetch_map(&map_w13);
+        tma_prefetch_map(&map_x);
+        tma_prefetch_map(&map_w2);
+        tma_prefetch_map(&map_h);
+    }
     if (threadIdx.x == 0) {
         S->dead = 0;
         for (int i = 0; i < p.stages; ++i) {
