@@ -293,3 +293,44 @@ def test_prompt_through_a_lut_layer(B, orc):
                           + x[:16].double().abs() @ sw.double().repeat_interleave(128, 0)[:300].repeat_interleave(128, 1).t())
     assert bool(((y[:16].double() - y16.double()).abs() <= (2 * 2.0 ** -4 + 2.0 ** -7) * bound + 1.1 * slack).all())
     layer.close()
+
+
+@pytest.mark.parametrize("m", [3, 200])
+def test_offsets_beyond_32_bits(B, m):
+    """Pitches that put rows of x, codes, scales and y more than 2^32 bytes apart."""
+    gen = torch.Generator().manual_seed(16)
+    n, k = 64, 300
+    ld_x = (1 << 32) // 2 // m + 64  # the last rows of x lie beyond 2^32 bytes
+    x_big = torch.empty((m + 1) * ld_x, dtype=torch.bfloat16, device="cuda")
+    x = x_big.view(m + 1, ld_x)[:m, :k]
+    x.copy_(torch.randn((m, k), generator=gen))
+    ld_q = (1 << 32) // m // 16 * 16 + 64
+    q = torch.empty((m + 1) * ld_q, dtype=torch.uint8, device="cuda").view(E4M3).view(m + 1, ld_q)[:m, :k]
+    s = torch.empty((m + 1) * (ld_q // 4), device="cuda").view(m + 1, ld_q // 4)[:m, :3]
+    B.sqz_fp8_quantize(x, q=q, scale=s)
+    q_ref, s_ref = quantize_ref(x.cpu()[None], 1, E4M3)
+    assert torch.equal(s.cpu(), s_ref[0]) and same_codes(q.cpu(), q_ref[0])
+    w, sw = random_matrix(gen, n, k, E4M3, 128)
+    y = torch.empty((m + 1) * (ld_q // 4), device="cuda").view(m + 1, ld_q // 4)[:m, :n]
+    B.sqz_fp8_gemm(q, s, w, sw, y)
+    check_product(y, q, s, w, sw)
+
+
+def test_two_streams_at_once(B):
+    gen = torch.Generator().manual_seed(17)
+    jobs = []
+    for m, n, k in ((5, 2000, 3000), (300, 1000, 3000), (64, 700, 1000), (1000, 800, 600)):
+        a, sa = random_matrix(gen, m, k, E4M3, 1)
+        w, sw = random_matrix(gen, n, k, E4M3, 128)
+        want = torch.empty((m, n), device="cuda")
+        B.sqz_fp8_gemm(a, sa, w, sw, want)
+        check_product(want, a, sa, w, sw)
+        jobs.append((a, sa, w, sw, torch.zeros_like(want), want, torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for a, sa, w, sw, y, _, stream in jobs:
+            B.sqz_fp8_gemm(a, sa, w, sw, y, stream=stream)
+    torch.cuda.synchronize()
+    for *_, y, want, _ in jobs:
+        assert torch.equal(y, want)
+    assert B.sqz_fp8_status() == 0

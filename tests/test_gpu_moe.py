@@ -305,3 +305,41 @@ def test_forward_refusals(B):
             B.sqz_moe_forward(moe, x, y, **bad)
     with pytest.raises(ValueError):
         B.sqz_moe_forward(moe, x.bfloat16(), y, workspace=ws)
+
+
+def test_experts_beyond_32_bits(B):
+    """Weights of more than 2^32 bytes: the last expert of many is the one expert of a small layer."""
+    experts, hidden, inter = 70, 8192, 4096
+    one = Case(1, hidden, inter, torch.bfloat16, seed=13)
+    x = one.x(2)
+    want = torch.empty_like(x)
+    small = one.handle(B, 1)
+    B.sqz_moe_forward(small, x, want, workspace=B.sqz_moe_workspace(small, 2))
+    f = dict(device="cuda")
+    w13 = torch.zeros((experts, 2 * inter, hidden), dtype=torch.uint8, **f).view(E4M3)
+    w2 = torch.zeros((experts, hidden, inter), dtype=torch.uint8, **f).view(E4M3)
+    s13 = torch.ones((experts, 2, inter // 128, hidden // 128), **f)
+    s2 = torch.ones((experts, hidden // 128, inter // 128), **f)
+    router = torch.zeros((experts, hidden), dtype=torch.bfloat16, **f)
+    w13[-1], s13[-1], w2[-1], s2[-1] = one.w13[0], one.s13[0], one.w2[0], one.s2[0]
+    router[-1] = x[0]
+    x2 = x[:1].repeat(2, 1)
+    big = B.sqz_create_moe(router, w13, s13, w2, s2, top_k=1)
+    ws = B.sqz_moe_workspace(big, 2)
+    y, ids = torch.empty_like(x2), torch.empty((2, 1), dtype=torch.int32, **f)
+    B.sqz_moe_forward(big, x2, y, ids=ids, workspace=ws)
+    assert B.sqz_moe_status(ws) == 0 and ids.flatten().tolist() == [experts - 1] * 2
+    fi = torch.finfo(torch.bfloat16)
+    for t in range(2):  # one rounding each; the sums are cut alike or not
+        assert bool(((y[t].double() - want[0].double()).abs() <= 2 * fi.eps * want[0].double().abs() + 1e-5).all())
+
+
+def test_padded_batch_and_repeated_rows(B):
+    """Rows behind the tokens of a call stay as they are; equal rows give equal results."""
+    case = Case(8, 256, 144, torch.float16, seed=14)
+    moe = case.handle(B, 2)
+    ws = B.sqz_moe_workspace(moe, 32)
+    x = case.x(1).repeat(9, 1)
+    y = torch.full((12, 256), 4.0, dtype=torch.float16, device="cuda")
+    B.sqz_moe_forward(moe, x, y[:9], workspace=ws)
+    assert bool((y[9:] == 4).all()) and all(torch.equal(y[0], y[t]) for t in range(1, 9))
