@@ -487,10 +487,9 @@ def sqz_fp8_quantize(x: torch.Tensor, block_rows: int = 1, dtype: torch.dtype = 
     block_rows (1 or 128) x 128; returns (q, scale).  q has x's shape and an fp8 dtype on a 16-byte row pitch;
     scale is [(batch,) ceil(rows / block_rows), ceil(cols / 128)].  Both are allocated unless given (q's dtype
     then names the format)."""
-    shape = x.shape
+    shape, dev = x.shape, _on_current_device(x, "x")
     if len(shape) not in (2, 3):
         raise ValueError("x must be [rows, cols] or [batch, rows, cols]")
-    dev = _on_current_device(x, "x")
     if x.dtype not in _H16_TYPES:
         raise TypeError(f"x has dtype {x.dtype}, expected fp16 or bf16")
     if block_rows not in (1, 128):
@@ -500,51 +499,50 @@ def sqz_fp8_quantize(x: torch.Tensor, block_rows: int = 1, dtype: torch.dtype = 
         if dtype not in _FP8_FORMATS:
             raise TypeError(f"dtype {dtype} is not an 8-bit floating-point type")
         q = torch.empty((*shape[:-1], (cols + 15) // 16 * 16), dtype=dtype, device=x.device)[..., :cols]
-    else:
-        _on_current_device(q, "q")
-        if q.dtype not in _FP8_FORMATS or q.shape != shape:
-            raise ValueError(f"q must have shape {tuple(shape)} and an fp8 dtype")
+    elif q.get_device() != dev or q.dtype not in _FP8_FORMATS or q.shape != shape:
+        raise ValueError(f"q must have shape {tuple(shape)} and an fp8 dtype, on x's device")
     s_shape = (*shape[:-2], -(-rows // block_rows), -(-cols // 128))
     if scale is None:
         scale = torch.empty(s_shape, dtype=torch.float32, device=x.device)
-    else:
-        _on_current_device(scale, "scale")
-        if scale.dtype != torch.float32 or scale.shape != s_shape:
-            raise ValueError(f"scale must be fp32 of shape {s_shape}")
-    if x.numel():
-        _check((_lib or lib()).sqz_fp8_quantize(
+    elif scale.get_device() != dev or scale.dtype is not torch.float32 or scale.shape != s_shape:
+        raise ValueError(f"scale must be fp32 of shape {s_shape}, on x's device")
+    if rows and cols and (len(shape) == 2 or shape[0]):
+        status = (_lib or lib()).sqz_fp8_quantize(
             x.data_ptr(), _TYPES[x.dtype], shape[0] if len(shape) == 3 else 1, rows, cols, _pitch(x, "x"), block_rows,
             _FP8_FORMATS[q.dtype], q.data_ptr(), _pitch(q, "q"), scale.data_ptr(), _pitch(scale, "scale"),
-            _raw_stream(stream, dev)), "sqz_fp8_quantize")
+            _raw_stream(stream, dev))
+        if status:
+            _check(status, "sqz_fp8_quantize")
     return q, scale
 
 
-def _fp8_matrix(q: torch.Tensor, scale: torch.Tensor, name: str, block_rows: int) -> sqz_fp8_matrix:
-    _on_current_device(q, name)
-    _on_current_device(scale, name)
-    if q.dtype not in _FP8_FORMATS:
+def _fp8_matrix(q: torch.Tensor, scale: torch.Tensor, name: str, block_rows: int, dev: int) -> sqz_fp8_matrix:
+    fmt, shape = _FP8_FORMATS.get(q.dtype), q.shape
+    if fmt is None:
         raise TypeError(f"{name} has dtype {q.dtype}, expected float8_e4m3fn or float8_e5m2")
-    shape = q.shape
-    if len(shape) != 2 or scale.dtype != torch.float32 or \
+    if q.get_device() != dev or scale.get_device() != dev:
+        raise ValueError(f"{name} and its scales must be on y's device")
+    if len(shape) != 2 or scale.dtype is not torch.float32 or \
             scale.shape != (-(-shape[0] // block_rows), -(-shape[1] // 128)):
         raise ValueError(f"{name} must be [rows, k] with fp32 scales [ceil(rows / {block_rows}), ceil(k / 128)], got "
                          f"{tuple(shape)} and {tuple(scale.shape)}")
-    return sqz_fp8_matrix(q.data_ptr(), _pitch(q, name), scale.data_ptr(), _pitch(scale, "scale"), _FP8_FORMATS[q.dtype])
+    return sqz_fp8_matrix(q.data_ptr(), _pitch(q, name), scale.data_ptr(), _pitch(scale, "scale"), fmt)
 
 
 def sqz_fp8_gemm(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor, y: torch.Tensor,
                  stream=None) -> None:
     """y [m, n] (fp16, bf16 or fp32) = A W^T of 8-bit matrices a [m, k] (scales [m, ceil(k/128)]) and w [n, k]
     (scales [ceil(n/128), ceil(k/128)])."""
-    A, W = _fp8_matrix(a, a_scale, "a", 1), _fp8_matrix(w, w_scale, "w", 128)
-    (m, k), (n, kw) = a.shape, w.shape
     dev = _on_current_device(y, "y")
+    A, W = _fp8_matrix(a, a_scale, "a", 1, dev), _fp8_matrix(w, w_scale, "w", 128, dev)
+    (m, k), (n, kw), y_type = a.shape, w.shape, _TYPES.get(y.dtype)
     if kw != k or y.shape != (m, n):
         raise ValueError(f"a {tuple(a.shape)}, w {tuple(w.shape)} and y {tuple(y.shape)} do not fit together")
-    if y.dtype not in _TYPES:
+    if y_type is None:
         raise TypeError(f"y has dtype {y.dtype}, expected fp16, bf16 or fp32")
-    _check((_lib or lib()).sqz_fp8_gemm(ctypes.byref(A), ctypes.byref(W), m, n, k, y.data_ptr(), _pitch(y, "y"),
-                                        _TYPES[y.dtype], _raw_stream(stream, dev)), "sqz_fp8_gemm")
+    status = (_lib or lib()).sqz_fp8_gemm(A, W, m, n, k, y.data_ptr(), _pitch(y, "y"), y_type, _raw_stream(stream, dev))
+    if status:
+        _check(status, "sqz_fp8_gemm")
 
 
 def sqz_fp8_status(stream=None) -> int:

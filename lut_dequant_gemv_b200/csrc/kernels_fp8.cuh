@@ -451,10 +451,10 @@ __global__ void __launch_bounds__(224) fp8_gemm_few_kernel(const __grid_constant
             if (t < tokens) red[t * 128 + r] = acc[t];
     }
     cluster_sync();
-    const int rows = 128 / splits;  // splits is a power of two
+    const int rows = (128 + splits - 1) / splits;  // that this CTA finishes
     for (int i = threadIdx.x; i < rows * tokens; i += S::kThreads) {
         const int t = i / rows, rr = rank * rows + i % rows;
-        if (row0 + rr >= p.n) continue;
+        if (rr >= 128 || row0 + rr >= p.n) continue;
         float v = 0.f;
         for (int c = 0; c < splits; ++c) v += ld_cluster(smem_u32(red + t * 128 + rr), c);
         store_out(p.y, (int64_t)(tok0 + t) * p.ldy + row0 + rr, p.out_type, v);

@@ -1,6 +1,8 @@
 // sqz_fp8.cu -- host side of the block-scaled 8-bit quantizer and matrix
 // product declared in include/sqz.h.  Every argument is checked on the host
 // before any CUDA call.
+#include <algorithm>
+
 #include "fp8_host.cuh"
 #include "kernels_fp8.cuh"
 
@@ -240,9 +242,12 @@ extern "C" SQZ_API sqz_status sqz_fp8_gemm(const sqz_fp8_matrix* a, const sqz_fp
         if ((st = tile_map(&mw, w->q, k, n, w->ld, 128)) != SQZ_OK) return st;
         if ((st = tile_map(&ma, a->q, k, m, a->ld, tb)) != SQZ_OK) return st;
         p.idesc = instr_desc(w->format, a->format, 128, tb);
-        // K split over up to 8 CTAs of a cluster until the grid fills the SMs
-        int splits = 1;
-        while (splits < 8 && 2 * splits <= p.nkb && row_blocks * splits * 2 <= 2 * d.sms) splits *= 2;
+        // K split over up to 8 CTAs of a cluster, while the grid stays within 7/8
+        // of the two CTAs an SM has room for: clusters do not fill the rest, and
+        // those left over run alone (16 x 5120 x 13824: 4, 6 and 7 CTAs 16.4,
+        // 16.6 and 24.5 us; 1 x 5120 x 5120: 8.1, 7.5 and 11.6 us).
+        int splits = (int)std::min<int64_t>(std::min(8, p.nkb), (int64_t)d.sms * 7 / 4 / row_blocks);
+        if (splits < 1) splits = 1;
         const int per_cta = (p.nkb + splits - 1) / splits;
         const int stage = tb * 128 + 16384 + (tb + 4) * 4;
         int stages = (d.smem / 2 - 4096) / stage;  // two CTAs share an SM
