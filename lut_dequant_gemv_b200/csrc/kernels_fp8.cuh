@@ -19,19 +19,23 @@ namespace f8 {
 // q0 - (q0 scale - x) y is x / scale correctly rounded (Markstein 1990) as
 // long as no step under- or overflows: three operations where a division
 // takes over ten (the kernel would be bound by them, not by its 3 bytes per
-// element).  Blocks whose scale is outside [2^-100, 2^120] (or NaN, or
-// infinite) divide.  Quotients below 2^-24 of the largest need no exactness:
-// they round to code 0 either way.
+// element).  The remainder q0 scale - x has bits down to 2^-47 of x, and a
+// quotient that does not round to code 0 is at least 2^-18, so scales from 2^-80
+// on keep it exact; blocks whose scale is outside [2^-80, 2^120] (or NaN, or
+// infinite) divide.
+//
+// Measured: 4096 x 13824 bf16 in 1 x 128 blocks 35 us, 4.9 TB/s (0.75 of the
+// copy rate), 11000 x 4100 fp16 in 128 x 128 blocks 30 us, 4.5 TB/s, a row of
+// 4096 1.7 us.  Bound by instructions (70 % of the issue slots, 16 an element),
+// half of them the quotients' and the maxima's.
 struct Quotient {
     float scale, inv;
     __device__ __forceinline__ explicit Quotient(float s) : scale(s), inv(1.f / s) {}
-    __device__ __forceinline__ bool divides() const { return !(scale >= 0x1p-100f && scale <= 0x1p120f); }
-    // Two quotients at once (packed fp32 instructions).  The remainder's sign
-    // is such that -0 / scale stays -0.
-    __device__ __forceinline__ void operator()(float& a, float& b) const {
-        const uint64_t x = pack2(-a, -b), ny = pack2(-inv, -inv);
-        const uint64_t q = mul2(x, ny), r = fma2_of(q, pack2(scale, scale), x);
-        unpack2(fma2_of(r, ny, q), a, b);
+    __device__ __forceinline__ bool divides() const { return !(scale >= 0x1p-80f && scale <= 0x1p120f); }
+    // (The remainder's sign is such that -0 / scale stays -0.)
+    __device__ __forceinline__ float operator()(float x) const {
+        const float q = x * inv;
+        return fmaf(-fmaf(q, scale, -x), inv, q);
     }
 };
 
@@ -113,9 +117,7 @@ __device__ __forceinline__ uint2 codes8(const Raw8& raw, const Quotient& by, boo
     } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            float a = x_to_float<BF16>(raw.w[i] & 0xFFFF), b = x_to_float<BF16>(raw.w[i] >> 16);
-            by(a, b);
-            w[i] = code2<E5M2>(a, b);
+            w[i] = code2<E5M2>(by(x_to_float<BF16>(raw.w[i] & 0xFFFF)), by(x_to_float<BF16>(raw.w[i] >> 16)));
         }
     }
     return make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
@@ -284,12 +286,16 @@ struct GemmParams {
 
 constexpr int kMaxStages = 12;
 
-// Few rows of A (up to 64): bound by reading W.  The weights
-// take the 128 lanes (MMA "A", 128 rows of W) and the TB tokens the columns,
-// so a tile costs the tensor cores little however few tokens there are, and
-// the K axis is split over the CTAs of a cluster, whose partial sums meet in
-// distributed shared memory in rank order: no workspace, no atomics, the same
-// bits every run.
+// Few rows of A (up to 64): bound by reading W.  The weights take the 128
+// lanes (MMA "A", 128 rows of W) and the TB tokens the columns, so a tile
+// costs the tensor cores little however few tokens there are, and the K axis
+// is split over the CTAs of a cluster, whose partial sums meet in distributed
+// shared memory in rank order: no workspace, no atomics, the same bits every
+// run.
+//
+// Measured: 16 x 5120 x 13824 16.6 us, 4.3 TB/s with about 4 us of launch,
+// first copies and the sums' meeting (16 x 18944 x 32768: 6.1 TB/s); 1 x 4096 x
+// 4096 6.1 us.
 //
 //   warp 0: TMA loads of W and A tiles into a ring of stages
 //   warp 1: TMEM allocation, matrix instructions into a ring of accumulators
@@ -301,8 +307,8 @@ struct FewShape {
     static constexpr int kScaleFloats = TB + 4;  // TB token scales, the weights' scale
     // A block's way from the matrix instruction through the promotion and back
     // to a free accumulator takes over a thousand cycles (barriers, mostly): two
-    // accumulators let a CTA do a block every 820, eight one every
-    // (half the tensor memory, so that two CTAs share an SM).
+    // accumulators let a CTA do a block every 820, eight one every 550 (half the
+    // tensor memory, so that two CTAs share an SM).
     static constexpr int kBufs = 256 / TB < 8 ? 256 / TB : 8;
     static constexpr int kTmemCols = kBufs * TB;
     static constexpr int kThreads = 224;
@@ -463,24 +469,30 @@ __global__ void __launch_bounds__(224) fp8_gemm_few_kernel(const __grid_constant
 }
 
 // Many rows of A: tiles of 256 rows of A x BN rows of W, by pairs of CTAs (one
-// CTA an SM, persistent).  What bounds a tile is first the way from L2: alone,
-// a CTA with a 128 x 256 tile takes 48 KB a block of K for 512 cycles of matrix
-// instructions and the SMs together get about 10 TB/s, which made a block take
-// over 1100 cycles whatever the promotion did.  In a pair each CTA loads its
-// own 128 rows of A and half of W's rows, 32 KB for the same work, and the
-// matrix instructions (cta_group::2) read W's halves from both.
+// CTA an SM, persistent): each CTA loads its own 128 rows of A and half of W's
+// rows, and the matrix instructions (cta_group::2) read W's halves from both.
+// Alone, a CTA with a 128 x 256 tile would have 48 KB a block of K written to
+// its shared memory and 48 KB read from it for 512 cycles of matrix
+// instructions, more than the 128 bytes a cycle it has.
 //
 // A thread of the promotion holds one row of A and BN / 2 columns: the block's
-// scale is then one number per thread (the row's scale times the scale of the
-// 128 rows of W that its columns lie in).  (Packed fp32 multiply-adds measured
-// slower here than plain ones.)
+// scale is then one or two numbers per thread (the row's scale times those of
+// the 128-row blocks of W that its columns lie in).  Packed fp32 multiply-adds
+// measured slower here than plain ones.
+//
+// What bounds it: the two accumulators of 256 columns fill tensor memory, so
+// an accumulator's whole way -- the matrix instructions (512 cycles, up to 950
+// while the promotion reads tensor memory), their completion's arrival (200),
+// the promotion's reads (480), the arrival that frees it (210) and the issue
+// (200) -- is paid once for every two blocks: 1080 cycles a block, 8192 x 11008
+// x 4096 in 357 us (2.07 PFLOP/s, tensor pipe 49 %; 420 us under the power cap).
 //
 //   warp 0: TMA ring (the full barriers live in the even CTA, the empty ones
 //   in both), warp 1: TMEM and, in the even CTA, matrix instructions, warp 2:
 //   scales, sixteen blocks of K ahead (a wait for each block's would cost the
-//   promotion 200 cycles of its 1000; loads into its registers stall its reads
-//   of tensor memory), warps 3-10: promotion (warp % 4 = the 32 lanes it may read; first or
-//   second half of the columns)
+//   promotion 200 cycles; loads into its registers stall its reads of tensor
+//   memory), warps 3-10: promotion (warp % 4 = the 32 lanes it may read; first
+//   or second half of the columns)
 template <int BN>
 struct ManyShape {
     static constexpr int kRowsW = BN / 2;  // of W, in each CTA
@@ -681,7 +693,7 @@ __global__ void __launch_bounds__(ManyShape<BN>::kThreads, 1) fp8_gemm_many_kern
 #pragma unroll
                 for (int c = 0; c < S::kCols; c += S::kChunk) {
                     uint32_t d[S::kChunk];
-                    tmem_ld(lanes + buf * BN + c, d);
+                    tmem_ld16(lanes + buf * BN + c, d);
                     tmem_wait_ld(d);
                     if (c + S::kChunk == S::kCols) {  // the accumulator is read
                         tc_fence_before();
