@@ -238,26 +238,25 @@ __device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[16]) {
                  : "memory");
 }
 
-// 32 bytes to a row of `align`-byte alignment (32 or 16): whole sectors.
-__device__ __forceinline__ void st_global_32b(void* p, uint64_t a, uint64_t b, uint64_t c, uint64_t d, int align) {
+// 32 bytes to a row of `align`-byte alignment (32, 16, 8 or 4).
+__device__ __forceinline__ void st_global_32b(void* p, const uint32_t (&w)[8], int align) {
     if (align == 32) {
-        asm volatile("st.global.v4.b64 [%0], {%1, %2, %3, %4};" ::"l"(p), "l"(a), "l"(b), "l"(c), "l"(d) : "memory");
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]),
+                     "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                     : "memory");
+    } else if (align == 16) {
+        uint4* q = static_cast<uint4*>(p);
+        q[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        q[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    } else if (align == 8) {
+        uint2* q = static_cast<uint2*>(p);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) q[i] = make_uint2(w[2 * i], w[2 * i + 1]);
     } else {
-        asm volatile("st.global.v2.b64 [%0], {%1, %2};" ::"l"(p), "l"(a), "l"(b) : "memory");
-        asm volatile("st.global.v2.b64 [%0+16], {%1, %2};" ::"l"(p), "l"(c), "l"(d) : "memory");
+        uint32_t* q = static_cast<uint32_t*>(p);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) q[i] = w[i];
     }
-}
-
-// ------------------------------------------------------------ arithmetic
-__device__ __forceinline__ uint64_t pack2(float a, float b) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ uint64_t pack2u(uint32_t a, uint32_t b) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(a), "r"(b));
-    return r;
 }
 
 // -------------------------------------------------------------- clusters

@@ -510,32 +510,46 @@ struct ManyShape {
     static int smem_bytes(int stages) { return 1024 + stages * kStageBytes + 2 * kScaleRun * kScaleRows * 4; }
 };
 
-// N consecutive values to a row of y whose alignment is p.out_align (32 or 16).
+// The first `left` of N consecutive values to a row of y, 32 bytes at a time
+// where the row's alignment (p.out_align) and its end allow it.
 template <int N>
-__device__ __forceinline__ void store_row(const GemmParams& p, int64_t at, const float (&v)[N]) {
+__device__ __forceinline__ void store_row(const GemmParams& p, int64_t at, int left, const float (&v)[N]) {
+    const bool wide = p.out_align >= 4;
     if (p.out_type == kF32) {
-        float* y = static_cast<float*>(p.y) + at;
 #pragma unroll
-        for (int j = 0; j < N; j += 8)
-            st_global_32b(y + j, pack2(v[j], v[j + 1]), pack2(v[j + 2], v[j + 3]), pack2(v[j + 4], v[j + 5]),
-                          pack2(v[j + 6], v[j + 7]), p.out_align);
+        for (int j = 0; j < N; j += 8) {
+            if (wide && j + 8 <= left) {
+                uint32_t w[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(v[j + i]);
+                st_global_32b(static_cast<float*>(p.y) + at + j, w, p.out_align);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (j + i < left) static_cast<float*>(p.y)[at + j + i] = v[j + i];
+            }
+        }
     } else {
-        uint16_t* y = static_cast<uint16_t*>(p.y) + at;
 #pragma unroll
         for (int j = 0; j < N; j += 16) {
-            uint32_t w[8];
+            if (wide && j + 16 <= left) {
+                uint32_t w[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                if (p.out_type == kF16) {
-                    const __half2 h = __floats2half2_rn(v[j + 2 * i], v[j + 2 * i + 1]);
-                    w[i] = *reinterpret_cast<const uint32_t*>(&h);
-                } else {
-                    const __nv_bfloat162 h = __floats2bfloat162_rn(v[j + 2 * i], v[j + 2 * i + 1]);
-                    w[i] = *reinterpret_cast<const uint32_t*>(&h);
+                for (int i = 0; i < 8; ++i) {
+                    if (p.out_type == kF16) {
+                        const __half2 h = __floats2half2_rn(v[j + 2 * i], v[j + 2 * i + 1]);
+                        w[i] = *reinterpret_cast<const uint32_t*>(&h);
+                    } else {
+                        const __nv_bfloat162 h = __floats2bfloat162_rn(v[j + 2 * i], v[j + 2 * i + 1]);
+                        w[i] = *reinterpret_cast<const uint32_t*>(&h);
+                    }
                 }
+                st_global_32b(static_cast<uint16_t*>(p.y) + at + j, w, p.out_align);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    if (j + i < left) store_out(p.y, at + j + i, p.out_type, v[j + i]);
             }
-            st_global_32b(y + j, pack2u(w[0], w[1]), pack2u(w[2], w[3]), pack2u(w[4], w[5]), pack2u(w[6], w[7]),
-                          p.out_align);
         }
     }
 }
@@ -711,15 +725,7 @@ __global__ void __launch_bounds__(ManyShape<BN>::kThreads, 1) fp8_gemm_many_kern
                 }
             }
             if (!alive || row >= p.m) continue;
-            const int64_t at = row * p.ldy + col0;
-            const int left = p.n - col0;
-            if (p.out_align >= 16 && left >= S::kCols) {
-                store_row<S::kCols>(p, at, acc);
-            } else {
-#pragma unroll
-                for (int j = 0; j < S::kCols; ++j)
-                    if (j < left) store_out(p.y, at + j, p.out_type, acc[j]);
-            }
+            store_row<S::kCols>(p, row * p.ldy + col0, p.n - col0, acc);
         }
     }
     __syncwarp();  // one lane ran the role: the barrier counts whole warps

@@ -120,8 +120,8 @@ sqz_status launch_many(const CUtensorMap& mw, const CUtensorMap& ma, GemmParams 
     return SQZ_OK;
 }
 
-// Up to here the few-row kernel, above it the many-row kernel (4096 x 4096: 64
-// rows 10 us, 128 rows 34 us against 15).
+// Rows of a few-row kernel's token tile; up to here it takes the call whatever W
+// is (4096 x 4096: 64 rows 10 us, by the many-row kernel 13).
 constexpr int kFewRows = 64;
 
 sqz_status check_matrix(const sqz_fp8_matrix* x, const char* name, int64_t rows, int32_t k) {
@@ -237,17 +237,33 @@ extern "C" SQZ_API sqz_status sqz_fp8_gemm(const sqz_fp8_matrix* a, const sqz_fp
     if ((st = status_word(&p.status)) != SQZ_OK) return st;
     CUtensorMap mw, ma;
     const int64_t row_blocks = ((int64_t)n + 127) / 128;
-    if (m <= kFewRows && row_blocks <= 65535) {
-        const int tb = round_pow2(m);
+    // Many rows: the width of the tiles with the least rounds of the pairs of SMs
+    // times a tile's time for a block of K, which measured 0.29, 0.35 and 0.56 us
+    // for 64, 128 and 256 columns: about 180 + 1.5 width ns.
+    const int64_t tm = (m + 255) / 256, pairs = d.sms / 2;
+    int bn = 256;
+    int64_t many = INT64_MAX;
+    for (int width : {256, 192, 160, 128, 64}) {
+        const int64_t tiles = tm * (((int64_t)n + width - 1) / width);
+        const int64_t ns = 5000 + (tiles + pairs - 1) / pairs * p.nkb * (180 + width * 3 / 2);
+        if (ns < many) many = ns, bn = width;
+    }
+    // Few rows: K split over up to 8 CTAs of a cluster, while the grid stays
+    // within 7/8 of the two CTAs an SM has room for: clusters do not fill the
+    // rest, and those left over run alone (16 x 5120 x 13824: 4, 6 and 7 CTAs
+    // 16.4, 16.6 and 24.5 us; 1 x 5120 x 5120: 8.1, 7.5 and 11.6 us).
+    const int tb = m < kFewRows ? round_pow2(m) : kFewRows;
+    const int64_t blocks = row_blocks * ((m + tb - 1) / tb);
+    int splits = (int)std::min<int64_t>(std::min(8, p.nkb), (int64_t)d.sms * 7 / 4 / blocks);
+    if (splits < 1) splits = 1;
+    // Beyond 64 rows the few-row kernel serves products with so little W that the
+    // many-row kernel's pairs would stand idle (it does not split K): a CTA's block
+    // of K takes about 480 ns (100 x 300 x 13824: 36 us, 12 split).
+    const int64_t few = 6000 + (blocks * splits + d.sms - 1) / d.sms * ((p.nkb + splits - 1) / splits) * 480;
+    if ((m <= kFewRows || few < many) && row_blocks <= 65535) {
         if ((st = tile_map(&mw, w->q, k, n, w->ld, 128)) != SQZ_OK) return st;
         if ((st = tile_map(&ma, a->q, k, m, a->ld, tb)) != SQZ_OK) return st;
         p.idesc = instr_desc(w->format, a->format, 128, tb);
-        // K split over up to 8 CTAs of a cluster, while the grid stays within 7/8
-        // of the two CTAs an SM has room for: clusters do not fill the rest, and
-        // those left over run alone (16 x 5120 x 13824: 4, 6 and 7 CTAs 16.4,
-        // 16.6 and 24.5 us; 1 x 5120 x 5120: 8.1, 7.5 and 11.6 us).
-        int splits = (int)std::min<int64_t>(std::min(8, p.nkb), (int64_t)d.sms * 7 / 4 / row_blocks);
-        if (splits < 1) splits = 1;
         const int per_cta = (p.nkb + splits - 1) / splits;
         const int stage = tb * 128 + 16384 + (tb + 4) * 4;
         int stages = (d.smem / 2 - 4096) / stage;  // two CTAs share an SM
@@ -259,17 +275,6 @@ extern "C" SQZ_API sqz_status sqz_fp8_gemm(const sqz_fp8_matrix* a, const sqz_fp
             case 32: return launch_few<32>(mw, ma, p, splits, stages, d, s);
             default: return launch_few<64>(mw, ma, p, splits, stages, d, s);
         }
-    }
-    // The width of the tiles: the least rounds of the pairs of SMs times a
-    // tile's time for a block of K, which measured 0.29, 0.35 and 0.56 us for
-    // 64, 128 and 256 columns: about proportional to 120 + width.
-    const int64_t tm = (m + 255) / 256, pairs = d.sms / 2;
-    int bn = 256;
-    int64_t least = INT64_MAX;
-    for (int width : {256, 192, 160, 128, 64}) {
-        const int64_t tiles = tm * (((int64_t)n + width - 1) / width);
-        const int64_t cost = (tiles + pairs - 1) / pairs * (120 + width);
-        if (cost < least) least = cost, bn = width;
     }
     if ((st = tile_map(&mw, w->q, k, n, w->ld, bn / 2)) != SQZ_OK) return st;
     if ((st = tile_map(&ma, a->q, k, m, a->ld, 128)) != SQZ_OK) return st;

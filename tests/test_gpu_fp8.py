@@ -188,7 +188,7 @@ def test_product_strides(B, m, dtype):
     w, sw = random_matrix(gen, n, k, E4M3, 128, pitch_extra=32)
     sa_wide = torch.full((m, 9), float("nan"), device="cuda")
     sa_wide[:, :4] = sa
-    for off, ldy in ((0, 336), (1, 341)):
+    for off, ldy in ((0, 336), (0, 344), (4, 340), (2, 338), (1, 341)):  # rows aligned to 32 bytes .. one value
         buf = torch.full(((m + 2) * ldy + off,), -7.0, dtype=dtype, device="cuda")
         y = buf[off:].view(m + 2, ldy)
         B.sqz_fp8_gemm(a, sa_wide[:, :4], w, sw, y[:m, :n])
