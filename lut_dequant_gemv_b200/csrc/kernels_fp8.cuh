@@ -57,16 +57,18 @@ __device__ __forceinline__ float x_to_float(uint32_t h) {
 
 // Eight consecutive elements of a row from column c, as they are stored
 // (zeros past the edge).  ALIGN: the alignment in bytes that x and its pitch
-// have, so the width of the loads.
+// have, so the width of the loads; kWhole: 16, and no row ends inside a block
+// (the edge's tests were a tenth of the instructions).
+constexpr int kWhole = 32;
 struct Raw8 {
     uint32_t w[4];
 };
 template <int ALIGN>
 __device__ __forceinline__ Raw8 load8(const uint16_t* __restrict__ row, int c, int cols) {
     Raw8 v;
-    if (ALIGN > 2 && c + 8 <= cols) {
+    if (ALIGN == kWhole || (ALIGN > 2 && c + 8 <= cols)) {
         const char* p = reinterpret_cast<const char*>(row + c);
-        if (ALIGN == 16) {
+        if (ALIGN >= 16) {
             const uint4 u = ldg_stream_u128(p);
             v.w[0] = u.x, v.w[1] = u.y, v.w[2] = u.z, v.w[3] = u.w;
         } else if (ALIGN == 8) {
@@ -123,8 +125,9 @@ __device__ __forceinline__ uint2 codes8(const Raw8& raw, const Quotient& by, boo
     return make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
 }
 // Eight codes to columns c .. of a row (rows are 16-byte aligned).
+template <int ALIGN>
 __device__ __forceinline__ void store_codes(uint8_t* __restrict__ row, int c, int cols, const uint2& q) {
-    if (c + 8 <= cols) {
+    if (ALIGN == kWhole || c + 8 <= cols) {
         *reinterpret_cast<uint2*>(row + c) = q;
     } else {
 #pragma unroll
@@ -202,11 +205,11 @@ __global__ void __launch_bounds__(256) fp8_quantize_rows_kernel(const QuantParam
             uint8_t* q = p.q + row[i] * p.ldq;
             const bool divides = by.divides();
             const uint2 lo = codes8<BF16, E5M2>(v[i][0], by, divides), hi = codes8<BF16, E5M2>(v[i][1], by, divides);
-            if (c + 16 <= p.cols) {
+            if (ALIGN == kWhole || c + 16 <= p.cols) {
                 *reinterpret_cast<uint4*>(q + c) = make_uint4(lo.x, lo.y, hi.x, hi.y);
             } else {
-                store_codes(q, c, p.cols, lo);
-                store_codes(q, c + 8, p.cols, hi);
+                store_codes<ALIGN>(q, c, p.cols, lo);
+                store_codes<ALIGN>(q, c + 8, p.cols, hi);
             }
             if (part == 0) p.scale[row[i] * p.lds + b[i]] = s;
         }
@@ -251,8 +254,8 @@ __global__ void __launch_bounds__(256, 4) fp8_quantize_tiles_kernel(const QuantP
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const int r = r0 + 16 * i;
-            if (r < p.rows && c < p.cols)
-                store_codes(q + (int64_t)r * p.ldq, c, p.cols, codes8<BF16, E5M2>(v[i], by, divides));
+            if (r < p.rows && (ALIGN == kWhole || c < p.cols))
+                store_codes<ALIGN>(q + (int64_t)r * p.ldq, c, p.cols, codes8<BF16, E5M2>(v[i], by, divides));
         }
     };
     if (by.divides())

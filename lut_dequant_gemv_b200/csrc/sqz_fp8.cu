@@ -54,6 +54,7 @@ cudaError_t launch_quantize(const QuantParams& p, int block_rows, int sms, cudaS
 template <bool BF16, bool E5M2>
 cudaError_t launch_quantize(const QuantParams& p, int block_rows, int align, int sms, cudaStream_t s) {
     switch (align) {
+        case kWhole: return launch_quantize<BF16, E5M2, kWhole>(p, block_rows, sms, s);
         case 16: return launch_quantize<BF16, E5M2, 16>(p, block_rows, sms, s);
         case 8: return launch_quantize<BF16, E5M2, 8>(p, block_rows, sms, s);
         case 4: return launch_quantize<BF16, E5M2, 4>(p, block_rows, sms, s);
@@ -188,6 +189,7 @@ extern "C" SQZ_API sqz_status sqz_fp8_quantize(const void* x, int32_t x_type, in
     p.nblocks = nblocks;
     int align = 16;  // of every row
     while (align > 2 && (reinterpret_cast<uintptr_t>(x) % align || ldx * 2 % align)) align /= 2;
+    if (align == 16 && cols % 128 == 0) align = kWhole;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const bool bf16 = x_type == SQZ_TYPE_BF16, e5m2 = format == SQZ_FP8_E5M2;
     const cudaError_t e = bf16 ? e5m2 ? launch_quantize<true, true>(p, block_rows, align, d.sms, s)
