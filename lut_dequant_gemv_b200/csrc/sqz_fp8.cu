@@ -260,8 +260,9 @@ extern "C" SQZ_API sqz_status sqz_fp8_gemm(const sqz_fp8_matrix* a, const sqz_fp
     if (splits < 1) splits = 1;
     // Beyond 64 rows the few-row kernel serves products with so little W that the
     // many-row kernel's pairs would stand idle (it does not split K): a CTA's block
-    // of K takes about 480 ns (100 x 300 x 13824: 36 us, 12 split).
-    const int64_t few = 6000 + (blocks * splits + d.sms - 1) / d.sms * ((p.nkb + splits - 1) / splits) * 480;
+    // of K takes about 400 ns (100 x 300 x 13824: 39 us, 11 this way; 128 x 4096 x
+    // 4096: 13.1 and 11.5).
+    const int64_t few = 5000 + (blocks * splits + d.sms - 1) / d.sms * ((p.nkb + splits - 1) / splits) * 400;
     if ((m <= kFewRows || few < many) && row_blocks <= 65535) {
         if ((st = tile_map(&mw, w->q, k, n, w->ld, 128)) != SQZ_OK) return st;
         if ((st = tile_map(&ma, a->q, k, m, a->ld, tb)) != SQZ_OK) return st;
