@@ -238,24 +238,16 @@ __device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[16]) {
                  : "memory");
 }
 
-// 32 bytes to a row of `align`-byte alignment (32, 16, 8 or 4).
+// 32 bytes to a row of 32- or 16-byte alignment.
 __device__ __forceinline__ void st_global_32b(void* p, const uint32_t (&w)[8], int align) {
     if (align == 32) {
         asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]),
                      "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
                      : "memory");
-    } else if (align == 16) {
+    } else {
         uint4* q = static_cast<uint4*>(p);
         q[0] = make_uint4(w[0], w[1], w[2], w[3]);
         q[1] = make_uint4(w[4], w[5], w[6], w[7]);
-    } else if (align == 8) {
-        uint2* q = static_cast<uint2*>(p);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) q[i] = make_uint2(w[2 * i], w[2 * i + 1]);
-    } else {
-        uint32_t* q = static_cast<uint32_t*>(p);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) q[i] = w[i];
     }
 }
 

@@ -93,15 +93,15 @@ sqz_status launch_few(const CUtensorMap& mw, const CUtensorMap& ma, GemmParams p
     return SQZ_OK;
 }
 
-template <int BN>
+template <int BN, int V>
 sqz_status launch_many(const CUtensorMap& mw, const CUtensorMap& ma, GemmParams p, const DeviceSizes& d,
                        cudaStream_t s) {
     static std::atomic<uint64_t> ready;
-    const sqz_status st = allow_smem(fp8_gemm_many_kernel<BN>, d, &ready);
+    const sqz_status st = allow_smem(fp8_gemm_many_kernel<BN, V>, d, &ready);
     if (st != SQZ_OK) return st;
     p.tiles_m = (p.m + 255) / 256;
     p.tiles_n = (p.n + BN - 1) / BN;
-    const int stages = (d.smem - 2048 - ManyShape<BN>::smem_bytes(0)) / ManyShape<BN>::kStageBytes;
+    const int stages = (d.smem - 512 - ManyShape<BN>::smem_bytes(0)) / ManyShape<BN>::kStageBytes;  // 512: static
     p.stages = stages > 8 ? 8 : stages;
     const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n, pairs = d.sms / 2;
     cudaLaunchConfig_t cfg = {};
@@ -117,8 +117,20 @@ sqz_status launch_many(const CUtensorMap& mw, const CUtensorMap& ma, GemmParams 
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    SQZ_F8_TRY(cudaLaunchKernelEx(&cfg, fp8_gemm_many_kernel<BN>, mw, ma, p), "fp8 product launch");
+    SQZ_F8_TRY(cudaLaunchKernelEx(&cfg, fp8_gemm_many_kernel<BN, V>, mw, ma, p), "fp8 product launch");
     return SQZ_OK;
+}
+
+// By the alignment of y's rows: 16 bytes, or 4, 2 or 1 values (of up to 8 bytes) at once.
+template <int BN>
+sqz_status launch_many(const CUtensorMap& mw, const CUtensorMap& ma, const GemmParams& p, const DeviceSizes& d,
+                       cudaStream_t s) {
+    if (p.out_align >= 16) return launch_many<BN, 0>(mw, ma, p, d, s);
+    switch (p.out_align / (p.out_type == SQZ_TYPE_F32 ? 4 : 2)) {
+        case 4: return launch_many<BN, 4>(mw, ma, p, d, s);
+        case 2: return launch_many<BN, 2>(mw, ma, p, d, s);
+        default: return launch_many<BN, 1>(mw, ma, p, d, s);
+    }
 }
 
 // Rows of a few-row kernel's token tile; up to here it takes the call whatever W
