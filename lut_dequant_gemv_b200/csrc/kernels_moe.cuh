@@ -38,6 +38,15 @@
 // The weights' ring runs through phases 1 and 2 without a stop: the first
 // tiles of phase 2 are on their way while the CTA waits for the last h.
 //
+// Measured: 8 tokens, 128 experts, top 8, 4096/1408: 159 us for 894 MB (5.6
+// TB/s; 6.3 in phase 1); one token, 8 experts, top 2, 4096/11008: 66 us (4.1
+// TB/s); one token, 64 experts, top 6, 2048/1408: 34 us, of which the weights'
+// time is 8.  The rest is latency, and most of that is instructions that are not
+// in the cache the one time they run: routing 3.5 us after the first barrier, a
+// tile's end 5 us (the counter's round trip 1.5, the join 1.5 to 3, h and its
+// digits 0.5 to 3).  Code on those paths is kept short: unrolling the digits'
+// loop and the join made 32 tokens 8 % slower.
+//
 // Warps: 0 weights (TMA), 1 TMEM and matrix instructions, 2 digits of x or h
 // (TMA, four rows a token) and scales, 3 idle after phase 1's routing,
 // 4-11 promotion (phase 1: 4-7 gate rows, 8-11 up rows; phase 2: both halves
@@ -434,7 +443,7 @@ struct Shared {
     uint32_t taddr;
     uint64_t h_arrived;              // the CTA's last h is written and its arrival posted
     unsigned long long h_target;     // the barrier round of that arrival
-    int dead, last;
+    int dead, last, owners[2];
     int cuts[2][kMaxGrid + 1];       // units of the two products by CTA
     __align__(16) uint32_t max_bits[kMaxTokens][4];
 };
@@ -738,14 +747,22 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
             }
             ++it;
         };
+        // The CTAs that have the units [first, first + whole), for the join: looked
+        // up while the counter's answer is on its way.
+        const auto find_owners = [&](const int* cuts, int first, int whole) {
+            S->owners[0] = owner(cuts, first);
+            S->owners[1] = owner(cuts, first + whole - 1);
+        };
         // Whether the other CTAs' pieces of a tile are all there: then this CTA
         // completes it, and its own piece need not leave the SM.  (Asked for the
-        // tile a CTA ends inside of: the next CTA starts with the rest of it.)
-        const auto others_done = [&](int* counter, int len, int whole) {
+        // tile a CTA ends inside of, by one that has more units than the tile's
+        // rest: the next CTAs start with that.)
+        const auto others_done = [&](int* counter, int len, const int* cuts, int first, int whole) {
             bar_promotion();
             if (first_thread) {
                 int done;
                 asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(done) : "l"(counter) : "memory");
+                find_owners(cuts, first, whole);
                 S->last = done + len == whole;
                 if (S->last) *counter = 0;  // for the next call
             }
@@ -754,14 +771,17 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
         };
         // Adds `len` of a tile's `whole` units to its counter once the pieces
         // of all 256 threads are written; true for the CTA that completes it.
-        const auto is_last = [&](int* counter, int len, int whole) {
+        const auto is_last = [&](int* counter, int len, const int* cuts, int first, int whole) {
             bar_promotion();
-            if (first_thread) {  // its fence covers what the barrier has ordered before it
-                fence_gpu();
-                const int old = atomicAdd(counter, len);
+            if (first_thread) {  // its release covers what the barrier has ordered before it
+                int old;
+                asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], %2;"
+                             : "=r"(old)
+                             : "l"(counter), "r"(len)
+                             : "memory");
+                find_owners(cuts, first, whole);
                 S->last = old + len == whole;
                 if (S->last) *counter = 0;  // for the next call
-                fence_gpu();
             }
             bar_promotion();
             return S->last != 0;
@@ -778,28 +798,34 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
                 const float* sc = unit_ready();
                 const float sw = sc[kMaxTokens + group];
 #pragma unroll
-                for (int b = 0; b < 8; ++b)
-                    if (4 * b < n) promote4(acc[b], lanes + ((it & (bufs - 1)) * 2 + group) * cols + b * 16, sc + 4 * b, sw);
+                for (int b = 0; b < 8; ++b) {
+                    if (4 * b >= n) break;
+                    promote4(acc[b], lanes + ((it & (bufs - 1)) * 2 + group) * cols + b * 16, sc + 4 * b, sw);
+                }
                 unit_done();
             }
             // From here on in shared memory, token by token: [token][gate, up rows]
             float* own = sums + group * 128 + r;
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-                if (i < n) own[i * 256] = acc[i / 4][i % 4];
+            for (int b = 0; b < 8; ++b) {
+                if (4 * b >= n) break;  // (few tokens fetch few instructions)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (4 * b + i < n) own[(4 * b + i) * 256] = acc[b][i];
+            }
             bool mine = len == nkb1;
             if (!mine) {  // a piece: at the tile's start (then the CTA's last tile) or not (then its first)
                 const int slot = k0 > 0 ? 0 : 1;
-                mine = slot == 1 && others_done(p.cnt1 + tile, len, nkb1);
+                const int first = tile * nkb1;
+                mine = slot == 1 && u1b - u1a > nkb1 - len && others_done(p.cnt1 + tile, len, S->cuts[0], first, nkb1);
                 if (!mine) {
                     float* dst = p.part1 + (int64_t)(blockIdx.x * 2 + slot) * p.tokens * 256 + group * 128 + r;
 #pragma unroll 2
                     for (int i = 0; i < n; ++i) __stcg(dst + i * 256, own[i * 256]);
-                    mine = is_last(p.cnt1 + tile, len, nkb1);
+                    mine = is_last(p.cnt1 + tile, len, S->cuts[0], first, nkb1);
                 }
                 if (mine) {
-                    const int first = tile * nkb1, used = n * 256, c0 = owner(S->cuts[0], first);
-                    const int c1 = owner(S->cuts[0], first + nkb1 - 1);
+                    const int used = n * 256, c0 = S->owners[0], c1 = S->owners[1];
                     for (int i = pt * 4; i < used; i += 2048) {
                         Joined s;
                         s.v[0] = *reinterpret_cast<const float4*>(sums + i);
@@ -883,15 +909,15 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
             if (len == per) {
                 for (int i = pt * 4; i < used; i += 1024) store_y<BF16>(p, i / 128, rt * 128 + i % 128, met(i));
             } else {
-                bool mine = slot == 1 && others_done(p.cnt2 + rt, len, per);
+                const int first = rt * per;
+                bool mine = slot == 1 && u2b - u2a > per - len && others_done(p.cnt2 + rt, len, S->cuts[1], first, per);
                 if (!mine) {
                     float* dst = p.part2 + (int64_t)(blockIdx.x * 2 + slot) * used;
                     for (int i = pt * 4; i < used; i += 1024) __stcg(reinterpret_cast<float4*>(dst + i), met(i));
-                    mine = is_last(p.cnt2 + rt, len, per);
+                    mine = is_last(p.cnt2 + rt, len, S->cuts[1], first, per);
                 }
                 if (mine) {
-                    const int first = rt * per, c0 = owner(S->cuts[1], first);
-                    const int c1 = owner(S->cuts[1], first + per - 1);
+                    const int c0 = S->owners[0], c1 = S->owners[1];
                     for (int i = pt * 4; i < used; i += 2048) {
                         Joined s;
                         s.v[0] = met(i);
