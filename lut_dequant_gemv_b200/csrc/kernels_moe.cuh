@@ -755,8 +755,8 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
         };
         // Whether the other CTAs' pieces of a tile are all there: then this CTA
         // completes it, and its own piece need not leave the SM.  (Asked for the
-        // tile a CTA ends inside of, by one that has more units than the tile's
-        // rest: the next CTAs start with that.)
+        // tile a CTA ends inside of, when it had others before: the next CTAs start
+        // with that tile's rest.)
         const auto others_done = [&](int* counter, int len, const int* cuts, int first, int whole) {
             bar_promotion();
             if (first_thread) {
@@ -817,7 +817,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
             if (!mine) {  // a piece: at the tile's start (then the CTA's last tile) or not (then its first)
                 const int slot = k0 > 0 ? 0 : 1;
                 const int first = tile * nkb1;
-                mine = slot == 1 && u1b - u1a > nkb1 - len && others_done(p.cnt1 + tile, len, S->cuts[0], first, nkb1);
+                mine = slot == 1 && u1b - u1a > len && others_done(p.cnt1 + tile, len, S->cuts[0], first, nkb1);
                 if (!mine) {
                     float* dst = p.part1 + (int64_t)(blockIdx.x * 2 + slot) * p.tokens * 256 + group * 128 + r;
 #pragma unroll 2
@@ -910,7 +910,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
                 for (int i = pt * 4; i < used; i += 1024) store_y<BF16>(p, i / 128, rt * 128 + i % 128, met(i));
             } else {
                 const int first = rt * per;
-                bool mine = slot == 1 && u2b - u2a > per - len && others_done(p.cnt2 + rt, len, S->cuts[1], first, per);
+                bool mine = slot == 1 && u2b - u2a > len && others_done(p.cnt2 + rt, len, S->cuts[1], first, per);
                 if (!mine) {
                     float* dst = p.part2 + (int64_t)(blockIdx.x * 2 + slot) * used;
                     for (int i = pt * 4; i < used; i += 1024) __stcg(reinterpret_cast<float4*>(dst + i), met(i));
