@@ -517,30 +517,39 @@ def sqz_fp8_quantize(x: torch.Tensor, block_rows: int = 1, dtype: torch.dtype = 
 
 
 def _fp8_matrix(q: torch.Tensor, scale: torch.Tensor, name: str, block_rows: int, dev: int) -> sqz_fp8_matrix:
-    fmt, shape = _FP8_FORMATS.get(q.dtype), q.shape
+    fmt = _FP8_FORMATS.get(q.dtype)
     if fmt is None:
         raise TypeError(f"{name} has dtype {q.dtype}, expected float8_e4m3fn or float8_e5m2")
     if q.get_device() != dev or scale.get_device() != dev:
         raise ValueError(f"{name} and its scales must be on y's device")
-    if len(shape) != 2 or scale.dtype is not torch.float32 or \
-            scale.shape != (-(-shape[0] // block_rows), -(-shape[1] // 128)):
-        raise ValueError(f"{name} must be [rows, k] with fp32 scales [ceil(rows / {block_rows}), ceil(k / 128)], got "
-                         f"{tuple(shape)} and {tuple(scale.shape)}")
-    return sqz_fp8_matrix(q.data_ptr(), _pitch(q, name), scale.data_ptr(), _pitch(scale, "scale"), fmt)
+    if q.dim() != 2 or scale.dim() != 2 or scale.dtype is not torch.float32:
+        raise ValueError(f"{name} must be [rows, k] with 2-D fp32 scales")
+    (rows, k), (srows, blocks), (ld, inner), (lds, sinner) = q.shape, scale.shape, q.stride(), scale.stride()
+    if srows != -(-rows // block_rows) or blocks != -(-k // 128):
+        raise ValueError(f"{name} {tuple(q.shape)} needs scales [ceil(rows / {block_rows}), ceil(k / 128)], got "
+                         f"{tuple(scale.shape)}")
+    if (inner != 1 and k > 1) or (sinner != 1 and blocks > 1):
+        raise ValueError(f"{name} and its scales must be row-major")
+    return sqz_fp8_matrix(q.data_ptr(), ld if rows > 1 else (k + 15) // 16 * 16, scale.data_ptr(),
+                          lds if srows > 1 else blocks, fmt)
 
 
 def sqz_fp8_gemm(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor, y: torch.Tensor,
                  stream=None) -> None:
     """y [m, n] (fp16, bf16 or fp32) = A W^T of 8-bit matrices a [m, k] (scales [m, ceil(k/128)]) and w [n, k]
     (scales [ceil(n/128), ceil(k/128)])."""
-    dev = _on_current_device(y, "y")
+    dev, y_type = _on_current_device(y, "y"), _TYPES.get(y.dtype)
     A, W = _fp8_matrix(a, a_scale, "a", 1, dev), _fp8_matrix(w, w_scale, "w", 128, dev)
-    (m, k), (n, kw), y_type = a.shape, w.shape, _TYPES.get(y.dtype)
+    (m, k), (n, kw) = a.shape, w.shape
     if kw != k or y.shape != (m, n):
         raise ValueError(f"a {tuple(a.shape)}, w {tuple(w.shape)} and y {tuple(y.shape)} do not fit together")
     if y_type is None:
         raise TypeError(f"y has dtype {y.dtype}, expected fp16, bf16 or fp32")
-    status = (_lib or lib()).sqz_fp8_gemm(A, W, m, n, k, y.data_ptr(), _pitch(y, "y"), y_type, _raw_stream(stream, dev))
+    ldy, inner = y.stride()
+    if inner != 1 and n > 1:
+        raise ValueError("y must be row-major")
+    status = (_lib or lib()).sqz_fp8_gemm(A, W, m, n, k, y.data_ptr(), ldy if m > 1 else n, y_type,
+                                          _raw_stream(stream, dev))
     if status:
         _check(status, "sqz_fp8_gemm")
 

@@ -334,3 +334,33 @@ def test_two_streams_at_once(B):
     for *_, y, want, _ in jobs:
         assert torch.equal(y, want)
     assert B.sqz_fp8_status() == 0
+
+
+def test_binding_refusals(B):
+    f = dict(device="cuda")
+    a, w = torch.zeros((4, 256), dtype=E4M3, **f), torch.zeros((130, 256), dtype=E4M3, **f)
+    sa, sw, y = torch.ones((4, 2), **f), torch.ones((2, 2), **f), torch.full((4, 130), 3.0, **f)
+    for bad in (dict(a=a[:, :255]), dict(w=w[:, :128]), dict(sa=sa[:3]), dict(sw=sw[:1]), dict(sa=sa.half()),
+                dict(y=y[:, :129]), dict(y=y.t()), dict(y=y.double()), dict(a=a.cpu()), dict(sw=sw.cpu()),
+                dict(a=a.to(torch.float16)), dict(w=torch.zeros((256, 130), dtype=torch.uint8, **f).view(E4M3).t()),
+                dict(a=torch.zeros((4, 260), dtype=torch.uint8, **f).view(E4M3)[:, 2:258])):
+        v = dict(a=a, sa=sa, w=w, sw=sw, y=y)
+        v.update(bad)
+        with pytest.raises((ValueError, TypeError, B.SqzError)):
+            B.sqz_fp8_gemm(v["a"], v["sa"], v["w"], v["sw"], v["y"])
+    torch.cuda.synchronize()
+    assert bool((y == 3).all())
+    B.sqz_fp8_gemm(a[:1], sa[:1], w[:1], sw[:1], y[:1, :1])  # single rows: any pitch
+    assert float(y[0, 0]) == 0
+
+
+def test_status_refuses_a_capture_and_leaves_it_intact(B):
+    x, y = torch.ones(4, device="cuda"), torch.zeros(4, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        with pytest.raises(B.SqzError) as e:
+            B.sqz_fp8_status()
+        assert e.value.status == B.SQZ_ERR_UNSUPPORTED
+        y.add_(x)
+    graph.replay()
+    assert bool((y == 1).all())
