@@ -96,7 +96,8 @@ struct Params {
     Header* head;
     int* cnt1;       // [experts * tiles_i]
     int* cnt2;       // [tiles_h]
-    float* logits;   // [tokens][experts]
+    float* logits;     // [tokens][experts]
+    float* logits_lo;  // what rounding the logits to fp32 left out, the same way
     uint8_t* xq;     // [tokens][4][hpad]
     float* sx;       // [tokens][nkb_h]
     uint8_t* hq;     // [pairs][4][ipad]
@@ -114,7 +115,7 @@ __host__ __device__ inline int b_rows(int tokens) { return (kDigits * tokens + 1
 
 // Shared memory of the logits' shares and, later, of the warps' logit keys.
 __host__ __device__ inline int scratch_bytes(int tokens, int experts) {
-    const int keys = (tokens < kWarps ? tokens : kWarps) * experts * 4, share = kWarps * 32 * 4;
+    const int keys = (tokens < kWarps ? tokens : kWarps) * experts * 4, share = kWarps * 32 * 8;
     return ((keys > share ? keys : share) + 127) / 128 * 128;
 }
 
@@ -208,37 +209,49 @@ __device__ __forceinline__ void load_x8(const uint16_t* row, int c, const Params
 // The logits of expert e for tokens [t_begin, t_end): the warp's share of the
 // columns (runs of 256, 8 a lane), then the lanes' sums; lane t returns token
 // t's.
+// Products and sums are in fp64: the choice of experts is a comparison, and in
+// fp32 two logits closer than their sums' error would change places.
 // The expert's row is held in registers (two runs at a time), so a token costs
 // its own loads only; four tokens' sums cross the lanes together.
 template <bool BF16>
-__device__ __forceinline__ float logits_share(const Params& p, int e, int t_begin, int t_end, int warp,
-                                              int lane) {
+__device__ __forceinline__ double logits_share(const Params& p, int e, int t_begin, int t_end, int warp,
+                                               int lane) {
     const uint16_t* r = p.router + (int64_t)e * p.ld_router;
-    float mine = 0.f;
+    double mine = 0.;
     for (int c0 = warp * 256; c0 < p.hidden; c0 += 2 * kWarps * 256) {
-        const int ca = c0 + lane * 8, cb = ca + kWarps * 256;
-        float ra[8], rb[8];
-        load_x8<BF16>(r, ca, p, ra);
-        load_x8<BF16>(r, cb, p, rb);
-#pragma unroll 2
+        const int c[2] = {c0 + lane * 8, c0 + kWarps * 256 + lane * 8};
+        const int runs = c0 + kWarps * 256 < p.hidden ? 2 : 1;
+        double rd[2][8];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            float rf[8];
+            load_x8<BF16>(r, c[k], p, rf);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) rd[k][j] = rf[j];
+        }
+#pragma unroll 1
         for (int t0 = t_begin; t0 < t_end; t0 += 4) {
-            float s[4];
+            double s[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const uint16_t* x = p.x + (int64_t)min(t0 + i, t_end - 1) * p.ldx;
-                float xa[8], xb[8];
-                load_x8<BF16>(x, ca, p, xa);
-                load_x8<BF16>(x, cb, p, xb);
-                s[i] = 0.f;
+                s[i] = 0.;
+                if (t0 + i >= t_end) continue;
+                const uint16_t* x = p.x + (int64_t)(t0 + i) * p.ldx;
 #pragma unroll
-                for (int j = 0; j < 8; ++j) s[i] = fmaf(ra[j], xa[j], fmaf(rb[j], xb[j], s[i]));
+                for (int k = 0; k < 2; ++k) {
+                    if (k >= runs) break;
+                    float xf[8];
+                    load_x8<BF16>(x, c[k], p, xf);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) s[i] = fma(rd[k][j], (double)xf[j], s[i]);
+                }
             }
             // lanes 8 i .. 8 i + 7 end with token t0 + i
             const bool up2 = lane & 16, up1 = lane & 8;
-            float k0 = up2 ? s[2] : s[0], k1 = up2 ? s[3] : s[1];
+            double k0 = up2 ? s[2] : s[0], k1 = up2 ? s[3] : s[1];
             k0 += __shfl_xor_sync(0xffffffffu, up2 ? s[0] : s[2], 16);
             k1 += __shfl_xor_sync(0xffffffffu, up2 ? s[1] : s[3], 16);
-            float v = up1 ? k1 : k0;
+            double v = up1 ? k1 : k0;
             v += __shfl_xor_sync(0xffffffffu, up1 ? k0 : k1, 8);
 #pragma unroll
             for (int off = 4; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
@@ -298,6 +311,19 @@ __device__ __forceinline__ float key_logit(uint32_t k) {
     return k == 1u ? __int_as_float(0x7FFFFFFF) : __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
 }
 
+// Of the experts whose fp32 logits are the same, `key`: the one that has most
+// beyond it, the lowest index where that is equal too (the whole warp).
+__device__ __noinline__ uint32_t best_of_equals(const float* lo, const uint32_t* keys, uint32_t key, int experts,
+                                                int lane) {
+    uint32_t k = 0, at = 0xffffffffu;
+#pragma unroll 4
+    for (int e = lane; e < experts; e += 32) {
+        const uint32_t v = keys[e] == key ? logit_key(__ldcg(lo + e)) : 0;
+        if (v > k) k = v, at = e;
+    }
+    return __reduce_min_sync(0xffffffffu, k == __reduce_max_sync(0xffffffffu, k) ? at : 0xffffffffu);
+}
+
 // The choice of one token by one warp: top_k rounds of the warp's best
 // (highest logit, lowest index).  `keys`: the warp's copy, [experts].
 __device__ __forceinline__ void route_token(const Params& p, Routing* R, uint32_t* keys, int t, int lane) {
@@ -319,14 +345,18 @@ __device__ __forceinline__ void route_token(const Params& p, Routing* R, uint32_
 #pragma unroll 1
     for (int j = 0; j < p.top_k; ++j) {
         uint32_t k = 0, at = 0xffffffffu;
+        bool again = false;  // the lane has its best key more than once
 #pragma unroll 4
         for (int e = lane; e < p.experts; e += 32) {
             const uint32_t v = keys[e];
+            again = v == k || (again && v < k);
             if (v > k) k = v, at = e;
         }
         const uint32_t high = __reduce_max_sync(0xffffffffu, k);
-        const uint32_t e = __reduce_min_sync(0xffffffffu, k == high ? at : 0xffffffffu);
-        if (e == at) keys[e] = 0;
+        uint32_t e = __reduce_min_sync(0xffffffffu, k == high ? at : 0xffffffffu);
+        if (__any_sync(0xffffffffu, k == high && (again || at != e)) && high > 1u)
+            e = best_of_equals(p.logits_lo + t * p.experts, keys, high, p.experts, lane);
+        if ((int)(e & 31) == lane) keys[e] = 0;  // (the lane that reads it)
         if (lane == j) mine = high, mine_id = (int)e;
     }
     float w = lane < p.top_k ? expf(key_logit(mine) - top) / sum : 0.f;
@@ -514,7 +544,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
     }
     for (int e = threadIdx.x; e < p.experts; e += kThreads) R->mask[e] = 0;
     // ---- phase 0: logits and the digits of x
-    float* share = reinterpret_cast<float*>(scratch);  // [kWarps][32]
+    double* share = reinterpret_cast<double*>(scratch);  // [kWarps][32]
     for (int u = gridDim.x - 1 - blockIdx.x + gridDim.x * warp; u < p.tokens * nkb1; u += gridDim.x * kWarps)
         x_digits_unit<BF16>(p, u / nkb1, u % nkb1, lane);
     for (int u = blockIdx.x; u < p.experts * groups; u += gridDim.x) {
@@ -523,10 +553,12 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
         __syncthreads();
         const int t = t0 + threadIdx.x;
         if (t < t1) {
-            float v = 0.f;
+            double v = 0.;
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) v += share[w * 32 + t];
-            p.logits[t * p.experts + e] = v;
+            const float l = (float)v;
+            p.logits[t * p.experts + e] = l;
+            p.logits_lo[t * p.experts + e] = fabsf(l) < __int_as_float(0x7F800000) ? (float)(v - l) : 0.f;
         }
         __syncthreads();
     }

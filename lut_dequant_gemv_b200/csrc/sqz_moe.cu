@@ -35,7 +35,7 @@ struct Layout {
         };
         cnt1 = take((size_t)m.d.experts * m.tiles_i * 4);
         cnt2 = take((size_t)m.tiles_h * 4);
-        logits = take((size_t)tokens * m.d.experts * 4);
+        logits = take((size_t)tokens * m.d.experts * 8);
         xq = take((size_t)tokens * M::kDigits * m.tiles_h * 128);
         sx = take((size_t)tokens * m.tiles_h * 4);
         hq = take(pairs * M::kDigits * m.tiles_i * 128);
@@ -164,6 +164,7 @@ extern "C" SQZ_API sqz_status sqz_moe_forward(sqz_moe_t moe, const void* x, int3
     p.cnt1 = reinterpret_cast<int*>(w + L.cnt1);
     p.cnt2 = reinterpret_cast<int*>(w + L.cnt2);
     p.logits = reinterpret_cast<float*>(w + L.logits);
+    p.logits_lo = p.logits + (size_t)tokens * d.experts;
     p.xq = w + L.xq;
     p.sx = reinterpret_cast<float*>(w + L.sx);
     p.hq = w + L.hq;

@@ -343,3 +343,21 @@ def test_padded_batch_and_repeated_rows(B):
     y = torch.full((12, 256), 4.0, dtype=torch.float16, device="cuda")
     B.sqz_moe_forward(moe, x, y[:9], workspace=ws)
     assert bool((y[9:] == 4).all()) and all(torch.equal(y[0], y[t]) for t in range(1, 9))
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("tokens,hidden", [(1, 2048), (7, 272), (32, 4096)])
+def test_near_equal_logits_go_to_the_larger(B, tokens, hidden, dtype):
+    """Experts in pairs whose logits differ by 2^-24, less than fp32 holds of logits about 1: the later one of
+    each pair is the larger."""
+    case = Case(24, hidden, 32, dtype, seed=15)
+    x = case.x(tokens)
+    eps = torch.finfo(dtype).eps
+    case.router[:, 40] = 1
+    case.router[12:] = case.router[:12]
+    case.router[12:, 40] += eps
+    x[:, 40] = 2.0 ** -24 / eps
+    moe = case.handle(B, 10)
+    check(B, case, x, 10, moe=moe)
+    case.router[12:, 40] -= eps  # and equal ones to the earlier
+    check(B, case, x, 10, moe=moe)
