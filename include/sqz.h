@@ -433,8 +433,9 @@ typedef struct {
  *
  * Arithmetic: products of codes are summed over a block of 128 by the tensor
  * cores into fp32, the blocks' sums times the product of their two scales are
- * added in fp32, and y is rounded once.  Bitwise reproducible.  NaN codes or
- * scales make the outputs they enter NaN.
+ * added in fp32, and y is rounded once.  Scales may have any magnitude: where
+ * their product leaves fp32's normal numbers it is applied in two steps.
+ * Bitwise reproducible.  NaN codes or scales make the outputs they enter NaN.
  *
  * Errors: SQZ_ERR_INVALID_ARG (NULL, negative or too small sizes and pitches,
  * unknown formats or types, misaligned codes or y); SQZ_ERR_CUDA.  No

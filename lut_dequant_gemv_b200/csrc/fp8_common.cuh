@@ -21,6 +21,8 @@
 namespace sqz {
 namespace f8 {
 
+using tc::cp_async_commit;
+using tc::cp_async_wait;
 using tc::fence_mbar_init;
 using tc::fence_proxy_async;
 using tc::mbar_arrive;
@@ -238,6 +240,17 @@ __device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[16]) {
                  : "memory");
 }
 
+// The same columns written, and the wait for such writes.
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15, %16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
 // 32 bytes to a row of 32- or 16-byte alignment.
 __device__ __forceinline__ void st_global_32b(void* p, const uint32_t (&w)[8], int align) {
     if (align == 32) {
@@ -289,6 +302,34 @@ __device__ __forceinline__ float4 ld_cluster4(const float* p, uint32_t rank) {
                  : "r"(cluster_addr(p, rank))
                  : "memory");
     return v;
+}
+
+// ---------------------------------------------------------------- scales
+// A block's sum is scaled by the product of two scales.  Each of them may be
+// anything fp32 holds, so the product may lie outside fp32's normal numbers where
+// the scaled sum does not (sums are 2^-32 to 2^39, or 0).
+__device__ __forceinline__ bool in_range(float product) {
+    return fabsf(product) >= 0x1p-126f && fabsf(product) < __int_as_float(0x7F800000);
+}
+// Then sum a b = (sum * first) * s: `first` a power of two whose product with a
+// sum that matters is exact, s rounded once, as a b is elsewhere.
+struct ScalePair {
+    float s, first;
+};
+__device__ __forceinline__ ScalePair split_scales(float a, float b) {
+    const float inf = __int_as_float(0x7F800000), p = a * b;
+    const bool swap = fabsf(a) > fabsf(b);
+    const float lo = swap ? b : a, hi = swap ? a : b;
+    ScalePair r = {p, 1.f};
+    if (in_range(p) || lo == 0.f || !(fabsf(hi) < inf)) return r;  // zeros, infinities and NaN: as they are
+    if (fabsf(p) < 1.f) {  // |lo| < 2^-63
+        r.first = 0x1p-64f;
+        r.s = lo * 0x1p64f * hi;
+    } else {  // |hi| >= 2^64; s stays finite, so that a sum of 0 gives 0
+        r.first = 0x1p126f;
+        r.s = fminf(fmaxf(hi * 0x1p-126f * lo, -0x1.fffffep127f), 0x1.fffffep127f);
+    }
+    return r;
 }
 
 __device__ __forceinline__ void store_out(void* y, int64_t at, int type, float v) {

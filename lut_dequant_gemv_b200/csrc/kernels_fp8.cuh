@@ -2,6 +2,8 @@
 // 128 columns: the quantizer and the matrix product.
 #pragma once
 
+#include <type_traits>
+
 #include "fp8_common.cuh"
 
 namespace sqz {
@@ -269,7 +271,10 @@ __global__ void __launch_bounds__(256, 4) fp8_quantize_tiles_kernel(const QuantP
 // y[m][n] = sum_b sa[m][b] sw[n / 128][b] * (sum over the 128 k of block b of
 // a[m][k] w[n][k]).  The inner sum is four tcgen05 matrix instructions into
 // tensor memory; the outer one is carried in fp32 registers, one fused
-// multiply-add per output and block ("promotion").
+// multiply-add per output and block ("promotion").  Blocks with a product of
+// scales outside fp32's normal numbers take two factors (split_scales); the
+// question costs the few-row kernel's promotion 1 %, the many-row kernel's is
+// asked by the warp that copies the scales.
 
 struct GemmParams {
     const float* sa;
@@ -415,18 +420,38 @@ __global__ void __launch_bounds__(224) fp8_gemm_few_kernel(const __grid_constant
         for (int it = 0; it < nk; ++it) {
             const int buf = it % S::kBufs;
             bool ok = wait_alive(&full[st], ph, dead);  // the scales of the stage
-            ok = ok && wait_alive(&tfull[buf], (it / S::kBufs) & 1, dead);
-            if (!__all_sync(0xffffffffu, ok)) break;
-            tc_fence_after();
             const float* sc = scales + st * S::kScaleFloats;
             const float sw = sc[TB];
+            const float mine = tok0 + lane % TB < p.m ? sc[lane % TB] * sw : 1.f;
+            const float late = TB > 32 && tok0 + lane + 32 < p.m ? sc[(lane + 32) % TB] * sw : 1.f;
+            ok = ok && wait_alive(&tfull[buf], (it / S::kBufs) & 1, dead);
+            const bool plain = __all_sync(0xffffffffu, ok && in_range(mine) && (TB <= 32 || in_range(late)));
+            if (!plain && !__all_sync(0xffffffffu, ok)) break;
+            tc_fence_after();
+            if (plain) {
 #pragma unroll
-            for (int c = 0; c < TB; c += 16) {
-                uint32_t d[16];
-                tmem_ld16(lanes + buf * TB + c, d);
-                tmem_wait_ld(d);
+                for (int c = 0; c < TB; c += 16) {
+                    uint32_t d[16];
+                    tmem_ld16(lanes + buf * TB + c, d);
+                    tmem_wait_ld(d);
 #pragma unroll
-                for (int j = 0; j < 16; ++j) acc[c + j] = fmaf(__uint_as_float(d[j]), sc[c + j] * sw, acc[c + j]);
+                    for (int j = 0; j < 16; ++j)
+                        acc[c + j] = fmaf(__uint_as_float(d[j]), sc[c + j] * sw, acc[c + j]);
+                }
+            } else {  // lane t splits the scales of tokens t and t + 32
+                const ScalePair own = split_scales(sc[lane % TB], sw), own32 = split_scales(sc[(lane + 32) % TB], sw);
+#pragma unroll
+                for (int c = 0; c < TB; c += 16) {
+                    uint32_t d[16];
+                    tmem_ld16(lanes + buf * TB + c, d);
+                    tmem_wait_ld(d);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        const ScalePair& from = c + j < 32 ? own : own32;
+                        const float f = __shfl_sync(0xffffffffu, from.first, (c + j) & 31);
+                        acc[c + j] = fmaf(__uint_as_float(d[j]) * f, __shfl_sync(0xffffffffu, from.s, (c + j) & 31), acc[c + j]);
+                    }
+                }
             }
             tc_fence_before();
             __syncwarp();
@@ -636,6 +661,24 @@ __device__ __forceinline__ void store_row(const GemmParams& p, int64_t at, int l
     }
 }
 
+// The warp's lanes' sums in tensor memory times a factor: `first` before column
+// `split` (a multiple of 16), `later` from there on.  The rare path of odd scales:
+// in tensor memory and in a loop, so that it takes nothing from the registers
+// and the unrolled reads of the others (a branch among those costs them a third).
+__device__ __forceinline__ void scale_sums(uint32_t taddr, int cols, int split, float first, float later) {
+#pragma unroll 1
+    for (int c = 0; c < cols; c += 16) {
+        const float f = c < split ? first : later;
+        uint32_t d[16];
+        tmem_ld16(taddr + c, d);
+        tmem_wait_ld(d);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) d[j] = __float_as_uint(__uint_as_float(d[j]) * f);
+        tmem_st16(taddr + c, d);
+    }
+    tmem_wait_st();
+}
+
 // V: 0 for 16-byte aligned rows of y, else the values of a store (see above).
 template <int BN, int V>
 __global__ void __launch_bounds__(ManyShape<BN>::kThreads, 1) fp8_gemm_many_kernel(
@@ -645,7 +688,7 @@ __global__ void __launch_bounds__(ManyShape<BN>::kThreads, 1) fp8_gemm_many_kern
     __shared__ uint64_t full[kMaxStages], empty[kMaxStages], tfull[S::kBufs], tempty[S::kBufs];
     __shared__ uint64_t sfull[2], sempty[2];
     __shared__ uint32_t taddr_s;
-    __shared__ int dead_s;
+    __shared__ int dead_s, odd_s[2];  // odd_s: whether a run's scales take two factors
     uint8_t* ring = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
     float* scales = reinterpret_cast<float*>(ring + p.stages * S::kStageBytes);
     volatile int* dead = &dead_s;
@@ -665,7 +708,7 @@ __global__ void __launch_bounds__(ManyShape<BN>::kThreads, 1) fp8_gemm_many_kern
             mbar_init(&tempty[i], 2 * S::kPromotionWarps);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&sfull[i], 32);
+            mbar_init(&sfull[i], 1);
             mbar_init(&sempty[i], S::kPromotionWarps);
         }
         fence_mbar_init();
@@ -748,14 +791,41 @@ __global__ void __launch_bounds__(ManyShape<BN>::kThreads, 1) fp8_gemm_many_kern
                 // L1 a copy, whatever the pitch.  (What belongs to no row is never
                 // stored: any scale does.)
                 const int k = k0 + (lane & 15), at = (lane & 15) / 4 * 4 * S::kScaleRows + (lane & 3);
+                const int rows = min(128, p.m - (tm * 256 + rank * 128)), wb = tn * BN / 128 + lane / 16;
                 if (k < p.nkb) {
-                    const int first = tm * 256 + rank * 128, rows = min(128, p.m - first);
-                    for (int i = lane / 16; i < rows; i += 2)
-                        cp_async4(dst + at + 4 * i, p.sa + (int64_t)(first + i) * p.ld_sa + k);
-                    const int wb = tn * BN / 128 + lane / 16;
+                    const float* sa = p.sa + (int64_t)(tm * 256 + rank * 128) * p.ld_sa + k;
+                    for (int i = lane / 16; i < rows; i += 2) cp_async4(dst + at + 4 * i, sa + (int64_t)i * p.ld_sa);
                     if (wb < w_blocks) cp_async4(dst + at + 4 * (128 + lane / 16), p.sw + wb * p.ld_sw + k);
                 }
-                cp_async_arrive(&sfull[runs & 1]);
+                cp_async_commit();
+                cp_async_wait<0>();
+                __syncwarp();
+                // The least and the largest of each side's magnitudes (bits order as
+                // values): products that they keep in range need no second factor.
+                uint32_t least = __float_as_uint(1.f), most = least, least_w = least, most_w = least;
+                for (int i = lane; i < rows; i += 32) {
+#pragma unroll
+                    for (int q = 0; q < S::kScaleRun / 4; ++q) {
+                        const uint4 a = *reinterpret_cast<const uint4*>(dst + 4 * (q * S::kScaleRows + i));
+                        const uint32_t v[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            if (k0 + 4 * q + j < p.nkb)
+                                least = min(least, v[j] & 0x7FFFFFFFu), most = max(most, v[j] & 0x7FFFFFFFu);
+                    }
+                }
+                if (k < p.nkb && wb < w_blocks) {
+                    const uint32_t v = __float_as_uint(dst[at + 4 * (128 + lane / 16)]) & 0x7FFFFFFFu;
+                    least_w = min(least_w, v), most_w = max(most_w, v);
+                }
+                least = __reduce_min_sync(0xffffffffu, least), least_w = __reduce_min_sync(0xffffffffu, least_w);
+                most = __reduce_max_sync(0xffffffffu, most), most_w = __reduce_max_sync(0xffffffffu, most_w);
+                if (lane == 0) {
+                    odd_s[runs & 1] = !in_range(__uint_as_float(least) * __uint_as_float(least_w)) ||
+                                      !in_range(__uint_as_float(most) * __uint_as_float(most_w));
+                    mbar_arrive(&sfull[runs & 1]);
+                }
+                __syncwarp();
             }
         }
     } else {
@@ -776,18 +846,20 @@ __global__ void __launch_bounds__(ManyShape<BN>::kThreads, 1) fp8_gemm_many_kern
             float acc[S::kCols];
 #pragma unroll
             for (int j = 0; j < S::kCols; ++j) acc[j] = 0.f;
-            const float* sc = nullptr;
-            for (int kb = 0; kb < p.nkb; ++kb, ++it) {
+            // Block kb of the run whose scales are at sc; `odd`: with two factors.
+            const auto promote = [&](const float* sc, int kb, auto odd) {
                 const int buf = it % S::kBufs;
-                if (kb % S::kScaleRun == 0) {
-                    if (!(alive = wait_warp(&sfull[runs & 1], (runs >> 1) & 1, dead))) break;
-                    sc = scales + (runs & 1) * S::kScaleRun * S::kScaleRows;
-                }
-                const float* quad = sc + (kb % S::kScaleRun / 4) * 4 * S::kScaleRows + kb % 4;
-                const float s0 = quad[4 * r] * quad[4 * (128 + block)];
-                const float s1 = S::kOneBlock ? s0 : quad[4 * r] * quad[4 * (128 + 1)];
-                if (!(alive = wait_warp(&tfull[buf], (it / S::kBufs) & 1, dead))) break;
+                const float* quad = sc + kb / 4 * 4 * S::kScaleRows + kb % 4;
+                float s0 = quad[4 * r] * quad[4 * (128 + block)];
+                float s1 = S::kOneBlock ? s0 : quad[4 * r] * quad[4 * (128 + 1)];
+                if (!(alive = wait_warp(&tfull[buf], (it / S::kBufs) & 1, dead))) return;
                 tc_fence_after();
+                if (odd) {
+                    const ScalePair f0 = split_scales(quad[4 * r], quad[4 * (128 + block)]);
+                    const ScalePair f1 = S::kOneBlock ? f0 : split_scales(quad[4 * r], quad[4 * (128 + 1)]);
+                    s0 = f0.s, s1 = f1.s;
+                    scale_sums(lanes + buf * BN, S::kCols, S::kOneBlock ? S::kCols : split, f0.first, f1.first);
+                }
 #pragma unroll
                 for (int c = 0; c < S::kCols; c += S::kChunk) {
                     uint32_t d[S::kChunk];
@@ -802,11 +874,21 @@ __global__ void __launch_bounds__(ManyShape<BN>::kThreads, 1) fp8_gemm_many_kern
                     for (int j = 0; j < S::kChunk; ++j)
                         acc[c + j] = fmaf(__uint_as_float(d[j]), S::kOneBlock || c < split ? s0 : s1, acc[c + j]);
                 }
-                if ((kb + 1) % S::kScaleRun == 0 || kb + 1 == p.nkb) {
-                    __syncwarp();
-                    if (elect_one()) mbar_arrive(&sempty[runs & 1]);
-                    ++runs;
+                ++it;
+            };
+            for (int k0 = 0; k0 < p.nkb && alive; k0 += S::kScaleRun, ++runs) {
+                if (!(alive = wait_warp(&sfull[runs & 1], (runs >> 1) & 1, dead))) break;
+                const float* sc = scales + (runs & 1) * S::kScaleRun * S::kScaleRows;
+                const int len = min(S::kScaleRun, p.nkb - k0);
+                if (!odd_s[runs & 1]) {
+#pragma unroll 1
+                    for (int kb = 0; kb < len && alive; ++kb) promote(sc, kb, std::false_type());
+                } else {  // (a loop of its own: tests in the other one cost it 3 to 30 %)
+#pragma unroll 1
+                    for (int kb = 0; kb < len && alive; ++kb) promote(sc, kb, std::true_type());
                 }
+                __syncwarp();
+                if (elect_one()) mbar_arrive(&sempty[runs & 1]);
             }
             if (!alive) continue;
             if (V == 0) {

@@ -364,3 +364,63 @@ def test_status_refuses_a_capture_and_leaves_it_intact(B):
         y.add_(x)
     graph.replay()
     assert bool((y == 1).all())
+
+
+# shapes for the few-row kernel's three tile sizes and the many-row kernel, in and across W's blocks of rows
+SCALE_SHAPES = [(4, 333, 700), (20, 333, 700), (50, 333, 700), (700, 1000, 2200), (300, 5000, 2500)]
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("m,n,k", SCALE_SHAPES)
+def test_product_of_small_scales(B, m, n, k, dtype):
+    """Scales about 2^-72, whose products are below fp32's normal numbers while the results are not."""
+    gen = torch.Generator().manual_seed(18)
+    a, sa = random_matrix(gen, m, k, E4M3, 1)
+    w, sw = random_matrix(gen, n, k, E4M3, 128)
+    for q in (a, w):  # of one sign, so that the products' errors do not average out
+        q.view(torch.uint8).bitwise_and_(0x7F)
+    sa, sw = sa * 2.0 ** -65, sw * 2.0 ** -65  # (random_matrix: about 1/100)
+    y = torch.empty((m, n), dtype=dtype, device="cuda")
+    B.sqz_fp8_gemm(a, sa, w, sw, y)
+    check_product(y, a, sa, w, sw)
+
+
+@pytest.mark.parametrize("m,n,k", SCALE_SHAPES)
+def test_product_of_large_scales(B, m, n, k):
+    """Scales about 2^65 with the smallest codes: the scales' products are beyond fp32, the results are not, and a
+    row of zeros stays zero."""
+    gen = torch.Generator().manual_seed(19)
+
+    def few_codes(rows, block_rows):
+        q, s = random_matrix(gen, rows, k, E4M3, block_rows)
+        small = (torch.rand((rows, k), generator=gen) < 0.02) * torch.randint(1, 3, (rows, k), generator=gen)
+        q.view(torch.uint8).copy_((small + 128 * torch.randint(0, 2, (rows, k), generator=gen)).to(torch.uint8))
+        return q, s * 2.0 ** 71
+
+    (a, sa), (w, sw) = few_codes(m, 1), few_codes(n, 128)
+    a.view(torch.uint8)[1] = 0
+    y = torch.empty((m, n), device="cuda")
+    B.sqz_fp8_gemm(a, sa, w, sw, y)
+    check_product(y, a, sa, w, sw)
+    assert bool((y[1] == 0).all())
+
+
+@pytest.mark.parametrize("m,n,k", SCALE_SHAPES)
+def test_product_of_scales_of_every_size(B, m, n, k):
+    """Each row of A and each block of rows of W at its own power of two, so that products inside and outside
+    fp32's range stand side by side; a scale of zero makes its part zero."""
+    gen = torch.Generator().manual_seed(20)
+    a, sa = random_matrix(gen, m, k, E4M3, 1)
+    w, sw = random_matrix(gen, n, k, E4M3, 128)
+    for s in (sa, sw):
+        s *= torch.exp2(torch.randint(-78, 45, (s.shape[0], 1), generator=gen).float()).cuda()
+    sa[2, 1] = 0
+    y = torch.empty((m, n), device="cuda")
+    B.sqz_fp8_gemm(a, sa, w, sw, y)
+    # results below fp32's normal numbers are rounded to a step of 2^-149, once for each block
+    A, W = dense(a, sa, 1), dense(w, sw, 128)
+    ref, S = A @ W.t(), A.abs() @ W.abs().t()
+    blocks = sa.shape[1]
+    tol = (2.0 ** -16 + (blocks + 4) * 2.0 ** -24) * S + blocks * 2.0 ** -149
+    bad = ~((y.double() - ref).abs() <= tol)
+    assert not bool(bad.any()), (int(bad.sum()), bad.nonzero()[:4].tolist())
