@@ -496,6 +496,23 @@ __device__ __forceinline__ void promote4(float (&acc)[4], uint32_t taddr, const 
     }
 }
 
+// The same where a product of scales leaves fp32's normal numbers: lane t has
+// split those of token t of the unit (row0: the group's first).
+__device__ __forceinline__ void promote4_split(float (&acc)[4], uint32_t taddr, const ScalePair& own, int row0) {
+    uint32_t d[16];
+    tmem_ld16(taddr, d);
+    tmem_wait_ld(d);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float v = __uint_as_float(d[4 * i + 3]);
+        v = fmaf(v, 0.0625f, __uint_as_float(d[4 * i + 2]));
+        v = fmaf(v, 0.0625f, __uint_as_float(d[4 * i + 1]));
+        v = fmaf(v, 0.0625f, __uint_as_float(d[4 * i]));
+        const float first = __shfl_sync(0xffffffffu, own.first, row0 + i);
+        acc[i] = fmaf(v * first, __shfl_sync(0xffffffffu, own.s, row0 + i), acc[i]);
+    }
+}
+
 template <bool BF16>
 __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant__ CUtensorMap map_w13,
                                                           const __grid_constant__ CUtensorMap map_w2,
@@ -761,14 +778,21 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
         // Once a wait has given up, the warps stop waiting but keep step (they
         // meet at barriers); the results are then undefined.
         bool alive = true;
-        // Waits for unit `it`: its scales and its sums.  Returns the scales.
-        const auto unit_ready = [&]() -> const float* {
+        // Waits for unit `it`: its scales and its sums.  Returns the scales; `plain`:
+        // whether the products of the n tokens' and the weights' (w) stay in range.
+        bool plain = true;
+        const auto unit_ready = [&](int n, int w) -> const float* {
             const int slot = it % kScaleSlots;
-            if (alive)
-                alive = __all_sync(0xffffffffu, wait_alive(&S->sfull[slot], (it / kScaleSlots) & 1, dead) &&
-                                                    wait_alive(&S->tfull[it & (bufs - 1)], (it >> bufs_log) & 1, dead));
+            const float* sc = S->scale[slot];
+            if (alive) {
+                bool ok = wait_alive(&S->sfull[slot], (it / kScaleSlots) & 1, dead);
+                const float product = lane < n ? sc[lane] * sc[kMaxTokens + w] : 1.f;
+                ok = ok && wait_alive(&S->tfull[it & (bufs - 1)], (it >> bufs_log) & 1, dead);
+                plain = __all_sync(0xffffffffu, ok && in_range(product));
+                if (!plain) alive = __all_sync(0xffffffffu, ok);
+            }
             tc_fence_after();
-            return S->scale[slot];
+            return sc;
         };
         const auto unit_done = [&]() {
             tc_fence_before();
@@ -827,12 +851,20 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
 #pragma unroll
             for (int i = 0; i < 32; ++i) acc[i / 4][i % 4] = 0.f;
             for (int i = 0; i < len; ++i) {
-                const float* sc = unit_ready();
+                const float* sc = unit_ready(n, group);
                 const float sw = sc[kMaxTokens + group];
+                const uint32_t at = lanes + ((it & (bufs - 1)) * 2 + group) * cols;
+                if (plain) {
 #pragma unroll
-                for (int b = 0; b < 8; ++b) {
-                    if (4 * b >= n) break;
-                    promote4(acc[b], lanes + ((it & (bufs - 1)) * 2 + group) * cols + b * 16, sc + 4 * b, sw);
+                    for (int b = 0; b < 8; ++b) {
+                        if (4 * b >= n) break;
+                        promote4(acc[b], at + b * 16, sc + 4 * b, sw);
+                    }
+                } else {
+                    const ScalePair own = split_scales(sc[lane], sw);
+#pragma unroll
+                    for (int b = 0; b < 8; ++b)
+                        if (4 * b < n) promote4_split(acc[b], at + b * 16, own, 4 * b);
                 }
                 unit_done();
             }
@@ -911,12 +943,22 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
 #pragma unroll
                 for (int i = 0; i < 16; ++i) acc[i / 4][i % 4] = 0.f;
                 for (int i = 0; i < run; ++i) {
-                    const float* sc = unit_ready();
+                    const float* sc = unit_ready(n, 0);
                     const float sw = sc[kMaxTokens];
+                    const uint32_t at = lanes + (it & (bufs - 1)) * 2 * cols;
+                    if (plain) {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const int b = 2 * j + group;
-                        if (4 * b < n) promote4(acc[j], lanes + (it & (bufs - 1)) * 2 * cols + b * 16, sc + 4 * b, sw);
+                        for (int j = 0; j < 4; ++j) {
+                            const int b = 2 * j + group;
+                            if (4 * b < n) promote4(acc[j], at + b * 16, sc + 4 * b, sw);
+                        }
+                    } else {
+                        const ScalePair own = split_scales(sc[lane], sw);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const int b = 2 * j + group;
+                            if (4 * b < n) promote4_split(acc[j], at + b * 16, own, 4 * b);
+                        }
                     }
                     unit_done();
                 }

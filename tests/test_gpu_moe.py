@@ -361,3 +361,21 @@ def test_near_equal_logits_go_to_the_larger(B, tokens, hidden, dtype):
     check(B, case, x, 10, moe=moe)
     case.router[12:, 40] -= eps  # and equal ones to the earlier
     check(B, case, x, 10, moe=moe)
+
+
+@pytest.mark.parametrize("tokens", [1, 6, 32])
+def test_scales_whose_products_leave_the_normal_numbers(B, tokens):
+    """Weight scales so small (or, with weights of zero, so large) that their products with the activations' powers of
+    two are not normal fp32 numbers, where the results are.  Everything is positive, so that errors add up."""
+    case = Case(4, 512, 256, torch.bfloat16, seed=16)
+    for codes in (case.w13, case.w2):
+        codes.view(torch.uint8).bitwise_and_(0x7F)
+    gate, up_ = case.s13[:, 0].clone(), case.s13[:, 1].clone()
+    case.s13[:, 0], case.s13[:, 1] = gate * 2.0 ** -114, up_ * 2.0 ** 65 * 2.0 ** 65  # gate about 2^-124, up 2^120
+    check(B, case, case.x(tokens, 2.0 ** -14).abs(), 2)
+    case.s13[:, 0], case.s13[:, 1] = gate, up_ * 2.0 ** -108  # h about 2^-100, y about 2^-124
+    case.s2 *= 2.0 ** -28
+    check(B, case, case.x(tokens).abs(), 2)
+    case.w13.zero_()  # nothing times anything
+    case.s13.fill_(2.0 ** 124)
+    check(B, case, case.x(tokens, 2.0 ** 20), 2)
