@@ -445,11 +445,13 @@ SQZ_API sqz_status sqz_fp8_gemm(const sqz_fp8_matrix* a, const sqz_fp8_matrix* w
                                 void* y, int64_t ldy, int32_t y_type, void* stream);
 
 /*
- * Read and clear the current device's status word of sqz_fp8_gemm, ordered on
- * `stream` (synchronises it; refused with SQZ_ERR_UNSUPPORTED on a stream
- * under capture).  0 means every call so far completed normally; bit 0 (1)
- * means that a bounded wait inside a kernel gave up and y of that call is
- * undefined (the call then returns SQZ_ERR_TIMEOUT with *status set).
+ * Read the current device's status of sqz_fp8_gemm, ordered on `stream`
+ * (synchronises it; refused with SQZ_ERR_UNSUPPORTED on a stream under
+ * capture).  0 means that every call which the stream has completed ended
+ * normally; bit 0 (1) means that a bounded wait inside a kernel gave up since the
+ * last status call, on any stream of the device, and y of that call is undefined
+ * (returns SQZ_ERR_TIMEOUT with *status set).  Each such wait is reported by
+ * one status call, whatever runs beside it.
  * Errors: SQZ_ERR_INVALID_ARG, SQZ_ERR_UNSUPPORTED, SQZ_ERR_CUDA,
  * SQZ_ERR_TIMEOUT.
  */

@@ -283,7 +283,7 @@ struct GemmParams {
     int64_t ld_sw;
     void* y;
     int64_t ldy;
-    int* status;
+    uint32_t* status;
     int m, n, nkb;  // nkb = blocks of K
     int out_type;
     uint32_t idesc;
@@ -466,7 +466,7 @@ __global__ void __launch_bounds__(224) fp8_gemm_few_kernel(const __grid_constant
     __syncthreads();
     tc_fence_after();
     if (warp == 1) tmem_dealloc(taddr, S::kTmemCols);
-    if (threadIdx.x == 0 && *dead) atomicOr(p.status, 1);
+    if (threadIdx.x == 0 && *dead) atomicAdd(p.status, 1u);
 
     const int tokens = min(TB, p.m - tok0);
     const int r = (warp & 3) * 32 + lane;  // row of W in the tile (promotion warps)
@@ -903,7 +903,7 @@ __global__ void __launch_bounds__(ManyShape<BN>::kThreads, 1) fp8_gemm_many_kern
     cluster_sync();  // nothing of the other CTA is on its way here any more
     tc_fence_after();
     if (warp == 1) tmem_dealloc_pair(taddr, S::kTmemCols);
-    if (threadIdx.x == 0 && *dead) atomicOr(p.status, 1);
+    if (threadIdx.x == 0 && *dead) atomicAdd(p.status, 1u);
 }
 
 }  // namespace f8

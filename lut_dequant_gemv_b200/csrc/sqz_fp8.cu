@@ -5,19 +5,22 @@
 
 #include "fp8_host.cuh"
 #include "kernels_fp8.cuh"
+#include "timeouts.cuh"
 
 namespace {
 
 using namespace sqz::f8;
 
-// Set by a kernel whose bounded wait gave up; read and cleared by
-// sqz_fp8_status.  One word per GPU.
-__device__ int g_fp8_status;
+// Counts, on every GPU, the CTAs of products whose bounded wait gave up; read by
+// sqz_fp8_status, which reports each once.
+__device__ uint32_t g_fp8_timeouts;
+constexpr int kMaxDevices = 256;
+sqz::ReportedTimeouts g_reported[kMaxDevices];
 
-sqz_status status_word(int** out) {
+sqz_status timeout_count(uint32_t** out) {
     void* p = nullptr;
-    SQZ_F8_TRY(cudaGetSymbolAddress(&p, g_fp8_status), "cudaGetSymbolAddress(fp8 status)");
-    *out = static_cast<int*>(p);
+    SQZ_F8_TRY(cudaGetSymbolAddress(&p, g_fp8_timeouts), "cudaGetSymbolAddress(fp8 timeouts)");
+    *out = static_cast<uint32_t*>(p);
     return SQZ_OK;
 }
 
@@ -248,7 +251,7 @@ extern "C" SQZ_API sqz_status sqz_fp8_gemm(const sqz_fp8_matrix* a, const sqz_fp
     p.out_align = 32;
     while (p.out_align > 2 && (reinterpret_cast<uintptr_t>(y) % p.out_align || ldy * out_bytes % p.out_align))
         p.out_align /= 2;
-    if ((st = status_word(&p.status)) != SQZ_OK) return st;
+    if ((st = timeout_count(&p.status)) != SQZ_OK) return st;
     CUtensorMap mw, ma;
     const int64_t row_blocks = ((int64_t)n + 127) / 128;
     // Many rows: the width of the tiles with the least rounds of the pairs of SMs
@@ -312,16 +315,19 @@ extern "C" SQZ_API sqz_status sqz_fp8_status(void* stream, int32_t* status) {
     if (cap != cudaStreamCaptureStatusNone)
         return host_fail(SQZ_ERR_UNSUPPORTED, "the stream is being captured into a CUDA graph; reading the status "
                                               "synchronises, which a capture cannot contain");
-    int* word = nullptr;
-    const sqz_status st = status_word(&word);
+    int device = 0;
+    SQZ_F8_TRY(cudaGetDevice(&device), "cudaGetDevice");
+    if (device >= kMaxDevices) return host_fail(SQZ_ERR_UNSUPPORTED, "device %d: at most %d are told apart", device, kMaxDevices);
+    uint32_t* count = nullptr;
+    const sqz_status st = timeout_count(&count);
     if (st != SQZ_OK) return st;
-    int h = 0;
-    SQZ_F8_TRY(cudaMemcpyAsync(&h, word, sizeof h, cudaMemcpyDeviceToHost, s), "reading the status");
-    SQZ_F8_TRY(cudaMemsetAsync(word, 0, sizeof h, s), "clearing the status");
+    uint32_t h = 0;
+    SQZ_F8_TRY(cudaMemcpyAsync(&h, count, sizeof h, cudaMemcpyDeviceToHost, s), "reading the status");
     SQZ_F8_TRY(cudaStreamSynchronize(s), "reading the status");
-    *status = h;
-    if (h & 1)
-        return host_fail(SQZ_ERR_TIMEOUT, "a bounded device wait gave up (status 0x%x): y of the affected call is "
-                                          "undefined", h);
+    if (g_reported[device].take(h)) {
+        *status = 1;
+        return host_fail(SQZ_ERR_TIMEOUT, "a bounded device wait gave up (status 0x1): y of the affected call is "
+                                          "undefined");
+    }
     return SQZ_OK;
 }
