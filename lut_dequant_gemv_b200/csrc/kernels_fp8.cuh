@@ -66,27 +66,27 @@ struct Raw8 {
     uint32_t w[4];
 };
 template <int ALIGN>
-__device__ __forceinline__ Raw8 load8(const uint16_t* __restrict__ row, int c, int cols) {
+__device__ __forceinline__ Raw8 load8(const uint16_t* row, int c, int cols) {
     Raw8 v;
     if (ALIGN == kWhole || (ALIGN > 2 && c + 8 <= cols)) {
         const char* p = reinterpret_cast<const char*>(row + c);
         if (ALIGN >= 16) {
-            const uint4 u = ldg_stream_u128(p);
+            const uint4 u = ld_once_u128(p);
             v.w[0] = u.x, v.w[1] = u.y, v.w[2] = u.z, v.w[3] = u.w;
         } else if (ALIGN == 8) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const uint2 u = __ldg(reinterpret_cast<const uint2*>(p) + i);
+                const uint2 u = ld_u64(p + 8 * i);
                 v.w[2 * i] = u.x, v.w[2 * i + 1] = u.y;
             }
         } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) v.w[i] = __ldg(reinterpret_cast<const uint32_t*>(p) + i);
+            for (int i = 0; i < 4; ++i) v.w[i] = ld_u32(p + 4 * i);
         }
     } else {
         uint16_t h[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) h[i] = c + i < cols ? __ldg(row + c + i) : 0;
+        for (int i = 0; i < 8; ++i) h[i] = c + i < cols ? ld_u16(row + c + i) : 0;
 #pragma unroll
         for (int i = 0; i < 4; ++i) v.w[i] = h[2 * i] | (uint32_t)h[2 * i + 1] << 16;
     }

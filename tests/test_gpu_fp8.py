@@ -424,3 +424,31 @@ def test_product_of_scales_of_every_size(B, m, n, k):
     tol = (2.0 ** -16 + (blocks + 4) * 2.0 ** -24) * S + blocks * 2.0 ** -149
     bad = ~((y.double() - ref).abs() <= tol)
     assert not bool(bad.any()), (int(bad.sum()), bad.nonzero()[:4].tolist())
+
+
+@pytest.mark.parametrize("m,n", [(5, 1000), (40, 4096), (600, 2000)])
+def test_each_call_reads_what_the_call_before_it_wrote(B, m, n):
+    """Product, quantizer of its result, product of that, over and over in the same buffers without a pause:
+    the same bits as with every call waited for."""
+    gen = torch.Generator().manual_seed(21)
+    xs = [torch.randn((m, n), generator=gen).bfloat16().cuda() for _ in range(4)]
+    w, sw = random_matrix(gen, n, n, E4M3, 128)
+    sw *= n ** -0.5
+    q = torch.empty((m, (n + 15) // 16 * 16), dtype=E4M3, device="cuda")[:, :n]
+    s, y = torch.empty((m, -(-n // 128)), device="cuda"), torch.empty((m, n), dtype=torch.bfloat16, device="cuda")
+
+    def chain(x, wait):
+        for step in range(3):
+            B.sqz_fp8_quantize(y if step else x, q=q, scale=s)
+            wait()
+            B.sqz_fp8_gemm(q, s, w, sw, y)
+            wait()
+        out = [y.clone(), q.clone(), s.clone()]
+        wait()
+        return out
+
+    want = [chain(x, torch.cuda.synchronize) for x in xs]
+    for _ in range(10):
+        got = [chain(x, lambda: None) for x in xs]
+        for a, b in zip(want, got):
+            assert torch.equal(a[0], b[0]) and same_codes(a[1], b[1]) and torch.equal(a[2], b[2])
