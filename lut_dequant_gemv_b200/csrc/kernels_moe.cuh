@@ -744,6 +744,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
         if (u2a < u2b && alive) {
             bool ok = true;
             if (lane == 0) ok = wait_alive(&S->h_arrived, 0, dead) && grid_wait(p.head, S->h_target, dead);
+            __syncwarp();  // what lane 0 has acquired, for the lanes that read it (a vote orders no memory)
             alive = __all_sync(0xffffffffu, ok);
             fence_proxy_all();
         }
