@@ -508,7 +508,8 @@ SQZ_API sqz_status sqz_moe_workspace_bytes(sqz_moe_t moe, int32_t tokens, int64_
  * y [tokens][ldy] = the layer applied to x [tokens][ldx], asynchronously on
  * `stream`, on the device the handle was made on.  ids [tokens][top_k] and
  * weights [tokens][top_k] (either may be NULL) receive the chosen experts, in
- * the order of falling logits, and their g.
+ * the order of falling logits, and their g.  y may be x (all of x is read before
+ * any of y is written); otherwise nothing may overlap.
  *
  * workspace: device memory on a 256-byte boundary of at least
  * sqz_moe_workspace_bytes(moe, tokens) bytes, zeroed once before its first

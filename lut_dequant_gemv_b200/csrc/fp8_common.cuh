@@ -116,10 +116,11 @@ __device__ __forceinline__ void let_copies_land() {
     for (int i = 0; i < 100; ++i) __nanosleep(1000000);
 }
 
-// Loads of what the previous kernel of the stream may have written.  A kernel that
-// is launched early is there before that one has ended, so these are plain
-// loads (the non-coherent path is for memory that stays as it is as long as the
-// kernel lives), and volatile: they stay behind the wait for that kernel.
+// Loads of what the previous kernel of the stream may have written (a kernel that
+// is launched early is there before that one has ended), or of what this one
+// writes later: plain loads (the non-coherent path is for memory that stays as
+// it is as long as the kernel lives), and volatile, so that they stay behind
+// waits and before barriers.
 __device__ __forceinline__ uint16_t ld_u16(const void* p) {
     uint16_t v;
     asm volatile("ld.global.u16 %0, [%1];" : "=h"(v) : "l"(p));
@@ -133,6 +134,11 @@ __device__ __forceinline__ uint32_t ld_u32(const void* p) {
 __device__ __forceinline__ uint2 ld_u64(const void* p) {
     uint2 v;
     asm volatile("ld.global.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+    return v;
+}
+__device__ __forceinline__ uint4 ld_u128(const void* p) {
+    uint4 v;
+    asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
     return v;
 }
 __device__ __forceinline__ uint4 ld_once_u128(const void* p) {  // read once: kept out of L1

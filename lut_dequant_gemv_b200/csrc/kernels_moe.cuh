@@ -120,8 +120,7 @@ __host__ __device__ inline int scratch_bytes(int tokens, int experts) {
 }
 
 template <bool BF16>
-__device__ __forceinline__ float load_x(const uint16_t* p) {
-    const uint16_t h = __ldg(p);
+__device__ __forceinline__ float to_float(uint16_t h) {
     return BF16 ? __uint_as_float((uint32_t)h << 16) : __half2float(__ushort_as_half(h));
 }
 
@@ -194,15 +193,19 @@ __device__ __forceinline__ void unpack8(const uint4& u, float (&v)[8]) {
         v[2 * j + 1] = BF16 ? __uint_as_float(w[j] & 0xFFFF0000u) : h2f((uint16_t)(w[j] >> 16));
     }
 }
-// Eight values from column c (zeros past `hidden`; a vector load when rows are
-// 16-byte aligned).
-template <bool BF16>
-__device__ __forceinline__ void load_x8(const uint16_t* row, int c, const Params& p, float (&v)[8]) {
+// Eight values from column c of a row of the router (zeros past `hidden`; a vector
+// load when rows are 16-byte aligned), or of x: plain loads, since y, which this
+// kernel writes later, may be x.
+template <bool BF16, bool X>
+__device__ __forceinline__ void load8(const uint16_t* row, int c, const Params& p, float (&v)[8]) {
     if (p.vec) {
-        unpack8<BF16>(c < p.hidden ? ldg_u128(row + c) : make_uint4(0, 0, 0, 0), v);
+        uint4 u = make_uint4(0, 0, 0, 0);
+        if (c < p.hidden) u = X ? ld_u128(row + c) : ldg_u128(row + c);
+        unpack8<BF16>(u, v);
     } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = c + j < p.hidden ? load_x<BF16>(row + c + j) : 0.f;
+        for (int j = 0; j < 8; ++j)
+            v[j] = c + j < p.hidden ? to_float<BF16>(X ? ld_u16(row + c + j) : __ldg(row + c + j)) : 0.f;
     }
 }
 
@@ -225,7 +228,7 @@ __device__ __forceinline__ double logits_share(const Params& p, int e, int t_beg
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
             float rf[8];
-            load_x8<BF16>(r, c[k], p, rf);
+            load8<BF16, false>(r, c[k], p, rf);
 #pragma unroll
             for (int j = 0; j < 8; ++j) rd[k][j] = rf[j];
         }
@@ -241,7 +244,7 @@ __device__ __forceinline__ double logits_share(const Params& p, int e, int t_beg
                 for (int k = 0; k < 2; ++k) {
                     if (k >= runs) break;
                     float xf[8];
-                    load_x8<BF16>(x, c[k], p, xf);
+                    load8<BF16, true>(x, c[k], p, xf);
 #pragma unroll
                     for (int j = 0; j < 8; ++j) s[i] = fma(rd[k][j], (double)xf[j], s[i]);
                 }
@@ -270,7 +273,7 @@ __device__ __forceinline__ void x_digits_unit(const Params& p, int t, int kb, in
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         const int c = kb * kBlockK + lane * 4 + j;
-        v[j] = c < p.hidden ? load_x<BF16>(p.x + (int64_t)t * p.ldx + c) : 0.f;
+        v[j] = c < p.hidden ? to_float<BF16>(ld_u16(p.x + (int64_t)t * p.ldx + c)) : 0.f;
         m = max(m, __float_as_uint(v[j]) & 0x7FFFFFFFu);
     }
     m = __reduce_max_sync(0xffffffffu, m);

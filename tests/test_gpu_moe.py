@@ -379,3 +379,20 @@ def test_scales_whose_products_leave_the_normal_numbers(B, tokens):
     case.w13.zero_()  # nothing times anything
     case.s13.fill_(2.0 ** 124)
     check(B, case, case.x(tokens, 2.0 ** 20), 2)
+
+
+@pytest.mark.parametrize("tokens,aligned", [(1, True), (9, False), (32, True)])
+def test_in_place(B, tokens, aligned):
+    """y may be x."""
+    case = Case(16, 512, 384, torch.bfloat16, seed=17)
+    moe = case.handle(B, 4)
+    ws = B.sqz_moe_workspace(moe, tokens)
+    x = case.x(tokens)
+    want = check(B, case, x, 4, moe=moe)
+    at = 0 if aligned else 1
+    buf = torch.zeros(tokens * 512 + at, dtype=torch.bfloat16, device="cuda")
+    for _ in range(3):
+        both = buf[at:].view(tokens, 512)
+        both.copy_(x)
+        B.sqz_moe_forward(moe, both, both, workspace=ws)
+        assert torch.equal(both, want)
