@@ -457,6 +457,21 @@ SQZ_API sqz_status sqz_fp8_gemm(const sqz_fp8_matrix* a, const sqz_fp8_matrix* w
  */
 SQZ_API sqz_status sqz_fp8_status(void* stream, int32_t* status);
 
+/*
+ * How sqz_fp8_gemm would cut a product on a device with the given SM count --
+ * computed on the host, no device needed.  many_rows = 0: the kernel for few rows
+ * of A, tiles of tile_rows (16, 32 or 64) rows of A by 128 rows of W, the
+ * blocks of K of each shared by a cluster of `splits` CTAs.  many_rows = 1: the
+ * kernel for many, tiles of 256 rows of A by tile_cols (64, 128, 160, 192 or
+ * 256) rows of W by pairs of CTAs, splits = 1.
+ * Errors: SQZ_ERR_INVALID_ARG for a NULL out, sizes below 1 or beyond
+ * 2^31 - 257, or sm_count < 2.
+ */
+typedef struct {
+    int32_t many_rows, tile_rows, tile_cols, splits;
+} sqz_fp8_plan_info;
+SQZ_API sqz_status sqz_fp8_plan_query(int32_t m, int32_t n, int32_t k, int32_t sm_count, sqz_fp8_plan_info* out);
+
 /* ------------------------------------------------ mixture of experts ---
  * A whole mixture-of-experts layer for a few tokens in one kernel launch:
  *

@@ -48,8 +48,8 @@ EXPORTED = ("sqz_create_layer", "sqz_gemv", "sqz_gemv_host", "sqz_debug_dequant"
             "sqz_destroy", "sqz_fp16_gemv", "sqz_last_error", "sqz_version", "sqz_check_csr_static",
             "sqz_layer_set_mac", "sqz_layer_set_csr_mode", "sqz_layer_status", "sqz_encode",
             "sqz_encode_outliers", "sqz_plan_query", "sqz_layer_set_predecode", "sqz_tile_split_query",
-            "sqz_fp8_quantize", "sqz_fp8_gemm", "sqz_fp8_status", "sqz_create_moe", "sqz_moe_workspace_bytes",
-            "sqz_moe_forward", "sqz_moe_status", "sqz_destroy_moe")
+            "sqz_fp8_quantize", "sqz_fp8_gemm", "sqz_fp8_status", "sqz_fp8_plan_query", "sqz_create_moe",
+            "sqz_moe_workspace_bytes", "sqz_moe_forward", "sqz_moe_status", "sqz_destroy_moe")
 
 
 class SqzError(RuntimeError):
@@ -86,6 +86,10 @@ class sqz_fp8_matrix(ctypes.Structure):
         ("ld_scale", ctypes.c_int64),
         ("format", ctypes.c_int32),
     ]
+
+
+class sqz_fp8_plan_info(ctypes.Structure):
+    _fields_ = [(name, ctypes.c_int32) for name in ("many_rows", "tile_rows", "tile_cols", "splits")]
 
 
 class sqz_moe_desc(ctypes.Structure):
@@ -145,6 +149,8 @@ def lib() -> ctypes.CDLL:
         L.sqz_fp8_gemm.restype = ctypes.c_int
         L.sqz_fp8_status.argtypes = [P, ctypes.POINTER(i32)]
         L.sqz_fp8_status.restype = ctypes.c_int
+        L.sqz_fp8_plan_query.argtypes = [i32, i32, i32, i32, ctypes.POINTER(sqz_fp8_plan_info)]
+        L.sqz_fp8_plan_query.restype = ctypes.c_int
         L.sqz_create_moe.argtypes = [ctypes.POINTER(sqz_moe_desc), ctypes.POINTER(P)]
         L.sqz_moe_workspace_bytes.argtypes = [P, i32, ctypes.POINTER(i64)]
         L.sqz_moe_forward.argtypes = [P, P, i32, i64, P, i64, P, P, P, i64, P]
@@ -558,6 +564,13 @@ def sqz_fp8_status(stream=None) -> int:
     st = ctypes.c_int32(-1)
     _check(lib().sqz_fp8_status(_stream(stream), ctypes.byref(st)), "sqz_fp8_status")
     return int(st.value)
+
+
+def sqz_fp8_plan_query(m: int, n: int, k: int, sm_count: int = 148) -> dict:
+    """How sqz_fp8_gemm would cut a product (host computation; default: B200)."""
+    info = sqz_fp8_plan_info()
+    _check(lib().sqz_fp8_plan_query(m, n, k, sm_count, ctypes.byref(info)), "sqz_fp8_plan_query")
+    return {name: int(getattr(info, name)) for name, _ in sqz_fp8_plan_info._fields_}
 
 
 # ------------------------------------------------ mixture of experts

@@ -140,6 +140,45 @@ sqz_status launch_many(const CUtensorMap& mw, const CUtensorMap& ma, const GemmP
 // is (4096 x 4096: 64 rows 10 us, by the many-row kernel 13).
 constexpr int kFewRows = 64;
 
+// Which kernel takes a product, and how it cuts it.
+struct Plan {
+    bool many;       // many rows of A
+    int tile_w;      // many: columns of y a tile (rows of W); few: 128
+    int tile_a;      // many: 256; few: rows of A a tile, 16, 32 or 64
+    int splits;      // few: CTAs of a cluster that share K
+};
+
+Plan plan_product(int32_t m, int32_t n, int32_t k, int sms) {
+    const int nkb = (k + 127) / 128;
+    const int64_t row_blocks = ((int64_t)n + 127) / 128;
+    // Many rows: the width of the tiles with the least rounds of the pairs of SMs
+    // times a tile's time for a block of K, which measured 0.29, 0.35 and 0.56 us
+    // for 64, 128 and 256 columns: about 180 + 1.5 width ns.
+    const int64_t tm = ((int64_t)m + 255) / 256, pairs = std::max(1, sms / 2);
+    int bn = 256;
+    int64_t many = INT64_MAX;
+    for (int width : {256, 192, 160, 128, 64}) {
+        const int64_t tiles = tm * (((int64_t)n + width - 1) / width);
+        const int64_t ns = 5000 + (tiles + pairs - 1) / pairs * nkb * (180 + width * 3 / 2);
+        if (ns < many) many = ns, bn = width;
+    }
+    // Few rows: K split over up to 8 CTAs of a cluster, while the grid stays
+    // within 7/8 of the two CTAs an SM has room for: clusters do not fill the
+    // rest, and those left over run alone (16 x 5120 x 13824: 4, 6 and 7 CTAs
+    // 16.4, 16.6 and 24.5 us; 1 x 5120 x 5120: 8.1, 7.5 and 11.6 us).
+    const int tb = m < kFewRows ? round_pow2(m) : kFewRows;
+    const int64_t blocks = row_blocks * (((int64_t)m + tb - 1) / tb);
+    int splits = (int)std::min<int64_t>(std::min(8, nkb), (int64_t)sms * 7 / 4 / blocks);
+    if (splits < 1) splits = 1;
+    // Beyond 64 rows the few-row kernel serves products with so little W that the
+    // many-row kernel's pairs would stand idle (it does not split K): a CTA's block
+    // of K takes about 400 ns (100 x 300 x 13824: 39 us, 11 this way; 128 x 4096 x
+    // 4096: 13.1 and 11.5).
+    const int64_t few = 5000 + (blocks * splits + sms - 1) / sms * ((nkb + splits - 1) / splits) * 400;
+    if ((m <= kFewRows || few < many) && row_blocks <= 65535) return {false, 128, tb, splits};
+    return {true, bn, 256, 1};
+}
+
 sqz_status check_matrix(const sqz_fp8_matrix* x, const char* name, int64_t rows, int32_t k) {
     if (!x) return host_fail(SQZ_ERR_INVALID_ARG, "%s is NULL", name);
     if (x->format != SQZ_FP8_E4M3 && x->format != SQZ_FP8_E5M2)
@@ -253,32 +292,9 @@ extern "C" SQZ_API sqz_status sqz_fp8_gemm(const sqz_fp8_matrix* a, const sqz_fp
         p.out_align /= 2;
     if ((st = timeout_count(&p.status)) != SQZ_OK) return st;
     CUtensorMap mw, ma;
-    const int64_t row_blocks = ((int64_t)n + 127) / 128;
-    // Many rows: the width of the tiles with the least rounds of the pairs of SMs
-    // times a tile's time for a block of K, which measured 0.29, 0.35 and 0.56 us
-    // for 64, 128 and 256 columns: about 180 + 1.5 width ns.
-    const int64_t tm = (m + 255) / 256, pairs = d.sms / 2;
-    int bn = 256;
-    int64_t many = INT64_MAX;
-    for (int width : {256, 192, 160, 128, 64}) {
-        const int64_t tiles = tm * (((int64_t)n + width - 1) / width);
-        const int64_t ns = 5000 + (tiles + pairs - 1) / pairs * p.nkb * (180 + width * 3 / 2);
-        if (ns < many) many = ns, bn = width;
-    }
-    // Few rows: K split over up to 8 CTAs of a cluster, while the grid stays
-    // within 7/8 of the two CTAs an SM has room for: clusters do not fill the
-    // rest, and those left over run alone (16 x 5120 x 13824: 4, 6 and 7 CTAs
-    // 16.4, 16.6 and 24.5 us; 1 x 5120 x 5120: 8.1, 7.5 and 11.6 us).
-    const int tb = m < kFewRows ? round_pow2(m) : kFewRows;
-    const int64_t blocks = row_blocks * ((m + tb - 1) / tb);
-    int splits = (int)std::min<int64_t>(std::min(8, p.nkb), (int64_t)d.sms * 7 / 4 / blocks);
-    if (splits < 1) splits = 1;
-    // Beyond 64 rows the few-row kernel serves products with so little W that the
-    // many-row kernel's pairs would stand idle (it does not split K): a CTA's block
-    // of K takes about 400 ns (100 x 300 x 13824: 39 us, 11 this way; 128 x 4096 x
-    // 4096: 13.1 and 11.5).
-    const int64_t few = 5000 + (blocks * splits + d.sms - 1) / d.sms * ((p.nkb + splits - 1) / splits) * 400;
-    if ((m <= kFewRows || few < many) && row_blocks <= 65535) {
+    const Plan plan = plan_product(m, n, k, d.sms);
+    if (!plan.many) {
+        const int tb = plan.tile_a, splits = plan.splits;
         if ((st = tile_map(&mw, w->q, k, n, w->ld, 128)) != SQZ_OK) return st;
         if ((st = tile_map(&ma, a->q, k, m, a->ld, tb)) != SQZ_OK) return st;
         p.idesc = instr_desc(w->format, a->format, 128, tb);
@@ -294,6 +310,7 @@ extern "C" SQZ_API sqz_status sqz_fp8_gemm(const sqz_fp8_matrix* a, const sqz_fp
             default: return launch_few<64>(mw, ma, p, splits, stages, d, s);
         }
     }
+    const int bn = plan.tile_w;
     if ((st = tile_map(&mw, w->q, k, n, w->ld, bn / 2)) != SQZ_OK) return st;
     if ((st = tile_map(&ma, a->q, k, m, a->ld, 128)) != SQZ_OK) return st;
     p.idesc = instr_desc(a->format, w->format, 256, bn);
@@ -329,5 +346,20 @@ extern "C" SQZ_API sqz_status sqz_fp8_status(void* stream, int32_t* status) {
         return host_fail(SQZ_ERR_TIMEOUT, "a bounded device wait gave up (status 0x1): y of the affected call is "
                                           "undefined");
     }
+    return SQZ_OK;
+}
+
+extern "C" SQZ_API sqz_status sqz_fp8_plan_query(int32_t m, int32_t n, int32_t k, int32_t sm_count,
+                                                 sqz_fp8_plan_info* out) {
+    if (!out) return host_fail(SQZ_ERR_INVALID_ARG, "out is NULL");
+    *out = sqz_fp8_plan_info{};
+    if (m < 1 || n < 1 || k < 1 || m > INT32_MAX - 256 || n > INT32_MAX - 256 || k > INT32_MAX - 256)
+        return host_fail(SQZ_ERR_INVALID_ARG, "m=%d, n=%d or k=%d outside [1, 2^31 - 257]", m, n, k);
+    if (sm_count < 2) return host_fail(SQZ_ERR_INVALID_ARG, "sm_count=%d: at least 2 expected", sm_count);
+    const Plan p = plan_product(m, n, k, sm_count);
+    out->many_rows = p.many;
+    out->tile_rows = p.tile_a;
+    out->tile_cols = p.tile_w;
+    out->splits = p.splits;
     return SQZ_OK;
 }
