@@ -452,3 +452,46 @@ def test_each_call_reads_what_the_call_before_it_wrote(B, m, n):
         got = [chain(x, lambda: None) for x in xs]
         for a, b in zip(want, got):
             assert torch.equal(a[0], b[0]) and same_codes(a[1], b[1]) and torch.equal(a[2], b[2])
+
+
+@pytest.mark.parametrize("dtype,fmt", [(torch.float16, E4M3), (torch.bfloat16, E5M2)])
+@pytest.mark.parametrize("batch,rows,cols,extra", [
+    (1, 20011, 100, 0),    # one block a row: a lane's next block is four rows on
+    (1, 20011, 100, 1),
+    (1, 5000, 777, 0),     # rows at odd offsets
+    (1, 5000, 776, 2),     # rows on 4 bytes
+    (3, 1700, 650, 6),     # ... of a batch with a pitch, a count of blocks that is no multiple of anything
+    (1, 5000, 772, 0),     # on 8 bytes
+    (1, 9601, 256, 0),     # whole blocks, an odd number of them
+    (1, 4100, 13824, 0),   # more blocks than the grid takes in one step
+    (2, 2050, 13700, 4),   # the same with edges
+])
+def test_quantize_of_more_blocks_than_the_sms_hold_at_once(B, batch, rows, cols, extra, dtype, fmt):
+    """1 x 128 blocks beyond 128 for each SM take two blocks a lane and stride over the grid."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    assert batch * rows * -(-cols // 128) > 128 * sms
+    gen = torch.Generator().manual_seed(rows + cols + extra)
+    x = make_x(gen, (batch, rows, cols + extra), dtype, "wide")[:, :, :cols]
+    qb = torch.full((batch, rows, (cols + 15) // 16 * 16 + 16), 7, dtype=torch.uint8, device="cuda").view(fmt)
+    sb = torch.full((batch, rows, -(-cols // 128) + 1), -1.0, device="cuda")
+    xd = torch.empty((batch, rows, cols + extra), dtype=dtype, device="cuda")[:, :, :cols]
+    xd.copy_(x)
+    B.sqz_fp8_quantize(xd, 1, q=qb[:, :, :cols], scale=sb[:, :, :-1])
+    q_ref, s_ref = quantize_ref(x, 1, fmt)
+    assert torch.equal(sb[:, :, :-1].cpu(), s_ref) and same_codes(qb[:, :, :cols].cpu(), q_ref)
+    assert bool((qb.view(torch.uint8)[:, :, cols:] == 7).all()) and bool((sb[:, :, -1] == -1).all())
+
+
+@pytest.mark.parametrize("fmt", [E4M3, E5M2])
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("block_rows", [1, 128])
+def test_quantize_at_every_alignment_of_the_rows(B, block_rows, dtype, fmt):
+    """Rows on 16, 8, 4 and 2 bytes, by their pitch and by their start, whole blocks and edges."""
+    gen = torch.Generator().manual_seed(22)
+    for cols in (256, 331):
+        for off, ldx in ((0, 336), (8, 352), (0, 340), (4, 336), (0, 338), (2, 336), (6, 344), (0, 337), (1, 336), (3, 339)):
+            big = make_x(gen, (off + 131 * ldx,), dtype, "wide")
+            x = big.cuda()[off:].view(131, ldx)[:, :cols]
+            q, s = B.sqz_fp8_quantize(x, block_rows, fmt)
+            q_ref, s_ref = quantize_ref(big[off:].view(131, ldx)[:, :cols][None], block_rows, fmt)
+            assert torch.equal(s.cpu(), s_ref[0]) and same_codes(q.cpu(), q_ref[0]), (cols, off, ldx)
