@@ -539,7 +539,9 @@ SQZ_API sqz_status sqz_moe_workspace_bytes(sqz_moe_t moe, int32_t tokens, int64_
  * the largest of their block of 128 within 2^-29 of it) and h to 2^-19; sums are
  * in fp32; y is rounded once.  The logits are summed in fp64 and compared to
  * 48 bits, so near-equal ones keep their order; the softmax is in fp32.
- * Bitwise reproducible.  A token whose x or h is not finite, or whose logits
+ * Bitwise reproducible for the same batch; a token's row may differ in its last
+ * bits beside other tokens, since the work is cut by the experts they reach
+ * together.  A token whose x or h is not finite, or whose logits
  * hold a NaN or pass fp32's range, gets NaN; its ids stay in range.
  *
  * Errors: SQZ_ERR_INVALID_ARG (NULL, tokens outside [0, SQZ_MOE_MAX_TOKENS],

@@ -396,3 +396,24 @@ def test_in_place(B, tokens, aligned):
         both.copy_(x)
         B.sqz_moe_forward(moe, both, both, workspace=ws)
         assert torch.equal(both, want)
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+def test_each_token_alone_and_in_a_batch(B, dtype):
+    """The work is cut over the SMs by the experts the whole batch reaches, so a token's sums are added in another order
+    beside others: its row agrees within the bound, not bit for bit, and its routing is the same."""
+    case = Case(16, 512, 384, dtype, seed=18)
+    moe = case.handle(B, 4)
+    ws = B.sqz_moe_workspace(moe, 32)
+    x = case.x(20)
+    y, ids = torch.empty_like(x), torch.empty((20, 4), dtype=torch.int32, device="cuda")
+    weights = torch.empty((20, 4), device="cuda")
+    B.sqz_moe_forward(moe, x, y, ids=ids, weights=weights, workspace=ws)
+    ref, err, _, _ = case.reference(x, 4, True)
+    eps = torch.finfo(dtype).eps
+    tol = 2 * (err + (ref.abs() + err) * eps / 2 + (2.0 ** -25 if dtype == torch.float16 else 0))  # each side's
+    for t in range(20):
+        alone, i1, w1 = torch.empty_like(x[:1]), torch.empty_like(ids[:1]), torch.empty_like(weights[:1])
+        B.sqz_moe_forward(moe, x[t:t + 1], alone, ids=i1, weights=w1, workspace=ws)
+        assert torch.equal(i1, ids[t:t + 1]) and torch.equal(w1, weights[t:t + 1])
+        assert bool(((alone[0].double() - y[t].double()).abs() <= tol[t]).all())
