@@ -511,8 +511,8 @@ typedef struct {
 /*
  * Make a handle (host data only).  Errors: SQZ_ERR_INVALID_ARG for NULL
  * pointers, sizes outside the ranges above, codes not on a 16-byte boundary;
- * SQZ_ERR_UNSUPPORTED for 2^31 or more weight blocks; SQZ_ERR_OOM;
- * SQZ_ERR_CUDA.  On error *out is NULL.
+ * SQZ_ERR_UNSUPPORTED for hidden or inter above 2^30 or 2^31 or more weight
+ * blocks; SQZ_ERR_OOM; SQZ_ERR_CUDA.  On error *out is NULL.
  */
 SQZ_API sqz_status sqz_create_moe(const sqz_moe_desc* desc, sqz_moe_t* out);
 

@@ -66,6 +66,9 @@ extern "C" SQZ_API sqz_status sqz_create_moe(const sqz_moe_desc* desc, sqz_moe_t
     if (d.hidden < 16 || d.inter < 16 || d.hidden % 16 || d.inter % 16)
         return host_fail(SQZ_ERR_INVALID_ARG, "hidden=%d and inter=%d must be positive multiples of 16", d.hidden,
                          d.inter);
+    // (the kernel's column indexes are 32 bits and run past the end by up to a step of the CTA)
+    if (d.hidden > 1 << 30 || d.inter > 1 << 30)
+        return host_fail(SQZ_ERR_UNSUPPORTED, "hidden=%d or inter=%d too large (at most 2^30)", d.hidden, d.inter);
     if (d.x_type != SQZ_TYPE_F16 && d.x_type != SQZ_TYPE_BF16)
         return host_fail(SQZ_ERR_INVALID_ARG, "x_type=%d: fp16 or bf16 expected", d.x_type);
     if (d.renormalize != 0 && d.renormalize != 1)

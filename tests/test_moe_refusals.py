@@ -65,3 +65,12 @@ def test_binding_refuses_host_tensors():
     z = torch.zeros
     with pytest.raises(ValueError):
         B.sqz_create_moe(z(4, 256), z(4, 256, 256), z(4, 2, 1, 2), z(4, 256, 128), z(4, 2, 1), top_k=1)
+
+
+@pytest.mark.parametrize("kw", [dict(hidden=(1 << 31) - 16, ld_router=1 << 31, inter=16), dict(inter=(1 << 31) - 16, hidden=16),
+                                dict(hidden=(1 << 30) + 16, ld_router=1 << 31, inter=16)])
+def test_create_refuses_sizes_beyond_its_32_bit_columns(lib, kw):
+    """Columns are counted in 32 bits, in steps of the whole CTA and rounded up to blocks."""
+    out = ctypes.c_void_p()
+    assert lib.sqz_create_moe(ctypes.byref(desc(experts=1, top_k=1, **kw)), ctypes.byref(out)) == B.SQZ_ERR_UNSUPPORTED
+    assert out.value is None and "too large" in B.sqz_last_error()
