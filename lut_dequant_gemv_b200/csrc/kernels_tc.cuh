@@ -885,7 +885,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) gemv_fused_kernel(const 
                 for (int b = 0; b < CM; ++b)
                     if (SB || b < B) {
                         // x of column cc[j]: staged in shared memory, or (x in K chunks) from L2
-                        const uint16_t xv = PS == 1 ? xs[b * P.x_stride + cc[j]] : __ldg(p.x + b * p.ldx + cc[j]);
+                        const uint16_t xv = PS == 1 ? xs[b * P.x_stride + cc[j]] : p.x[b * p.ldx + cc[j]];
                         acc[b] = fmaf(v, h2f(xv), acc[b]);
                     }
             }
@@ -906,7 +906,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) gemv_fused_kernel(const 
 #pragma unroll
                 for (int b = 0; b < CM; ++b)
                     if (SB || b < B) {
-                        const uint16_t xv = PS == 1 ? xs[b * P.x_stride + cj] : __ldg(p.x + b * p.ldx + cj);
+                        const uint16_t xv = PS == 1 ? xs[b * P.x_stride + cj] : p.x[b * p.ldx + cj];
                         acc[b] = fmaf(v, h2f(xv), acc[b]);
                     }
             }

@@ -15,6 +15,8 @@ def test_kernels_launched_early_read_through_the_coherent_path():
     writes: not through the non-coherent path, which requires memory that nobody writes while the kernel lives."""
     for name in ("kernels_fp8.cuh", "fp8_common.cuh"):
         assert not re.search(r"__ldg\(|ldg_stream_u128|ldg_u128|ldg_u32|\.nc\b", code(name)), name
+    for name in ("kernels_tc.cuh", "kernels_pd.cuh"):  # (their weights never change)
+        assert not re.search(r"(__ldg|ldg_\w+)\(p\.x\b", code(name)), name
 
 
 def test_a_barrier_hands_on_what_one_thread_acquired_from_the_grid():
