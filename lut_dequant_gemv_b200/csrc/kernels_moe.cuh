@@ -483,36 +483,51 @@ struct Shared {
 
 __device__ __forceinline__ void bar_promotion() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
-// acc[i] += scale_i * sw * (four digits' columns) for the tokens of group b
-// (four tokens = 16 columns).
-__device__ __forceinline__ void promote4(float (&acc)[4], uint32_t taddr, const float* sc, float sw) {
-    uint32_t d[16];
-    tmem_ld16(taddr, d);
-    tmem_wait_ld(d);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        float v = __uint_as_float(d[4 * i + 3]);
-        v = fmaf(v, 0.0625f, __uint_as_float(d[4 * i + 2]));
-        v = fmaf(v, 0.0625f, __uint_as_float(d[4 * i + 1]));
-        v = fmaf(v, 0.0625f, __uint_as_float(d[4 * i]));
-        acc[i] = fmaf(v, sc[i] * sw, acc[i]);
-    }
+// The four digits' columns of four tokens joined (16 columns of tensor memory).
+__device__ __forceinline__ float joined(const uint32_t (&d)[16], int i) {
+    float v = __uint_as_float(d[4 * i + 3]);
+    v = fmaf(v, 0.0625f, __uint_as_float(d[4 * i + 2]));
+    v = fmaf(v, 0.0625f, __uint_as_float(d[4 * i + 1]));
+    return fmaf(v, 0.0625f, __uint_as_float(d[4 * i]));
 }
-
-// The same where a product of scales leaves fp32's normal numbers: lane t has
-// split those of token t of the unit (row0: the group's first).
-__device__ __forceinline__ void promote4_split(float (&acc)[4], uint32_t taddr, const ScalePair& own, int row0) {
+// acc[j][i] += scale * sw * sum for n tokens, groups of four from `first` on,
+// `step` apart: group first + step j in acc[j].  Whether the scales' products
+// (lane: token) stay in range is asked while tensor memory answers; if one does
+// not, lane t splits those of token t.
+template <int GROUPS>
+__device__ __forceinline__ void promote(float (&acc)[GROUPS][4], uint32_t taddr, const float* sc, float sw, int n,
+                                        int first, int step, int lane) {
+    if (4 * first >= n) return;
     uint32_t d[16];
-    tmem_ld16(taddr, d);
+    tmem_ld16(taddr + first * 16, d);
+    const bool plain = __all_sync(0xffffffffu, lane >= n || in_range(sc[lane] * sw));
     tmem_wait_ld(d);
+    if (plain) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        float v = __uint_as_float(d[4 * i + 3]);
-        v = fmaf(v, 0.0625f, __uint_as_float(d[4 * i + 2]));
-        v = fmaf(v, 0.0625f, __uint_as_float(d[4 * i + 1]));
-        v = fmaf(v, 0.0625f, __uint_as_float(d[4 * i]));
-        const float first = __shfl_sync(0xffffffffu, own.first, row0 + i);
-        acc[i] = fmaf(v * first, __shfl_sync(0xffffffffu, own.s, row0 + i), acc[i]);
+        for (int j = 0; j < GROUPS; ++j) {
+            const int b = first + j * step;
+            if (4 * b >= n) break;
+            if (j > 0) {
+                tmem_ld16(taddr + b * 16, d);
+                tmem_wait_ld(d);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[j][i] = fmaf(joined(d, i), sc[4 * b + i] * sw, acc[j][i]);
+        }
+    } else {
+        const ScalePair own = split_scales(sc[lane], sw);
+#pragma unroll
+        for (int j = 0; j < GROUPS; ++j) {
+            const int b = first + j * step;
+            if (4 * b < n) {
+                tmem_ld16(taddr + b * 16, d);
+                tmem_wait_ld(d);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    acc[j][i] = fmaf(joined(d, i) * __shfl_sync(0xffffffffu, own.first, 4 * b + i),
+                                     __shfl_sync(0xffffffffu, own.s, 4 * b + i), acc[j][i]);
+            }
+        }
     }
 }
 
@@ -782,21 +797,14 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
         // Once a wait has given up, the warps stop waiting but keep step (they
         // meet at barriers); the results are then undefined.
         bool alive = true;
-        // Waits for unit `it`: its scales and its sums.  Returns the scales; `plain`:
-        // whether the products of the n tokens' and the weights' (w) stay in range.
-        bool plain = true;
-        const auto unit_ready = [&](int n, int w) -> const float* {
+        // Waits for unit `it`: its scales and its sums.  Returns the scales.
+        const auto unit_ready = [&]() -> const float* {
             const int slot = it % kScaleSlots;
-            const float* sc = S->scale[slot];
-            if (alive) {
-                bool ok = wait_alive(&S->sfull[slot], (it / kScaleSlots) & 1, dead);
-                const float product = lane < n ? sc[lane] * sc[kMaxTokens + w] : 1.f;
-                ok = ok && wait_alive(&S->tfull[it & (bufs - 1)], (it >> bufs_log) & 1, dead);
-                plain = __all_sync(0xffffffffu, ok && in_range(product));
-                if (!plain) alive = __all_sync(0xffffffffu, ok);
-            }
+            if (alive)
+                alive = __all_sync(0xffffffffu, wait_alive(&S->sfull[slot], (it / kScaleSlots) & 1, dead) &&
+                                                    wait_alive(&S->tfull[it & (bufs - 1)], (it >> bufs_log) & 1, dead));
             tc_fence_after();
-            return sc;
+            return S->scale[slot];
         };
         const auto unit_done = [&]() {
             tc_fence_before();
@@ -855,21 +863,8 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
 #pragma unroll
             for (int i = 0; i < 32; ++i) acc[i / 4][i % 4] = 0.f;
             for (int i = 0; i < len; ++i) {
-                const float* sc = unit_ready(n, group);
-                const float sw = sc[kMaxTokens + group];
-                const uint32_t at = lanes + ((it & (bufs - 1)) * 2 + group) * cols;
-                if (plain) {
-#pragma unroll
-                    for (int b = 0; b < 8; ++b) {
-                        if (4 * b >= n) break;
-                        promote4(acc[b], at + b * 16, sc + 4 * b, sw);
-                    }
-                } else {
-                    const ScalePair own = split_scales(sc[lane], sw);
-#pragma unroll
-                    for (int b = 0; b < 8; ++b)
-                        if (4 * b < n) promote4_split(acc[b], at + b * 16, own, 4 * b);
-                }
+                const float* sc = unit_ready();
+                promote(acc, lanes + ((it & (bufs - 1)) * 2 + group) * cols, sc, sc[kMaxTokens + group], n, 0, 1, lane);
                 unit_done();
             }
             // From here on in shared memory, token by token: [token][gate, up rows]
@@ -947,23 +942,8 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
 #pragma unroll
                 for (int i = 0; i < 16; ++i) acc[i / 4][i % 4] = 0.f;
                 for (int i = 0; i < run; ++i) {
-                    const float* sc = unit_ready(n, 0);
-                    const float sw = sc[kMaxTokens];
-                    const uint32_t at = lanes + (it & (bufs - 1)) * 2 * cols;
-                    if (plain) {
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const int b = 2 * j + group;
-                            if (4 * b < n) promote4(acc[j], at + b * 16, sc + 4 * b, sw);
-                        }
-                    } else {
-                        const ScalePair own = split_scales(sc[lane], sw);
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const int b = 2 * j + group;
-                            if (4 * b < n) promote4_split(acc[j], at + b * 16, own, 4 * b);
-                        }
-                    }
+                    const float* sc = unit_ready();
+                    promote(acc, lanes + (it & (bufs - 1)) * 2 * cols, sc, sc[kMaxTokens], n, group, 2, lane);
                     unit_done();
                 }
 #pragma unroll

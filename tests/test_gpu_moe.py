@@ -376,6 +376,9 @@ def test_scales_whose_products_leave_the_normal_numbers(B, tokens):
     case.s13[:, 0], case.s13[:, 1] = gate, up_ * 2.0 ** -108  # h about 2^-100, y about 2^-124
     case.s2 *= 2.0 ** -28
     check(B, case, case.x(tokens).abs(), 2)
+    case.s13[:, 0], case.s13[:, 1] = gate * 2.0 ** -51, up_ * 2.0 ** 121  # gate about 2^-123, h 2^-75
+    case.s2 *= 2.0 ** 68
+    check(B, case, case.x(tokens, 2.0 ** -75).abs(), 2)
     case.w13.zero_()  # nothing times anything
     case.s13.fill_(2.0 ** 124)
     check(B, case, case.x(tokens, 2.0 ** 20), 2)
