@@ -273,8 +273,8 @@ __global__ void __launch_bounds__(256, 4) fp8_quantize_tiles_kernel(const QuantP
 // tensor memory; the outer one is carried in fp32 registers, one fused
 // multiply-add per output and block ("promotion").  Blocks with a product of
 // scales outside fp32's normal numbers take two factors (split_scales); the
-// question costs the few-row kernel's promotion 1 %, the many-row kernel's is
-// asked by the warp that copies the scales.
+// few-row kernel's promotion asks while tensor memory answers, the many-row
+// kernel's leaves it to the warp that copies the scales.
 
 struct GemmParams {
     const float* sa;
@@ -416,33 +416,45 @@ __global__ void __launch_bounds__(224) fp8_gemm_few_kernel(const __grid_constant
 #pragma unroll
         for (int t = 0; t < TB; ++t) acc[t] = 0.f;
         const uint32_t lanes = taddr + ((uint32_t)(warp & 3) << 21);
+        const bool no_token = tok0 + lane % TB >= p.m, no_later = TB > 32 ? tok0 + lane + TB - 32 >= p.m : no_token;
         int st = 0, ph = 0;
         for (int it = 0; it < nk; ++it) {
             const int buf = it % S::kBufs;
             bool ok = wait_alive(&full[st], ph, dead);  // the scales of the stage
+            ok = ok && wait_alive(&tfull[buf], (it / S::kBufs) & 1, dead);
+            if (!__all_sync(0xffffffffu, ok)) break;
+            tc_fence_after();
             const float* sc = scales + st * S::kScaleFloats;
             const float sw = sc[TB];
-            const float mine = tok0 + lane % TB < p.m ? sc[lane % TB] * sw : 1.f;
-            const float late = TB > 32 && tok0 + lane + 32 < p.m ? sc[(lane + 32) % TB] * sw : 1.f;
-            ok = ok && wait_alive(&tfull[buf], (it / S::kBufs) & 1, dead);
-            const bool plain = __all_sync(0xffffffffu, ok && in_range(mine) && (TB <= 32 || in_range(late)));
-            if (!plain && !__all_sync(0xffffffffu, ok)) break;
-            tc_fence_after();
+            uint32_t d[16];
+            tmem_ld16(lanes + buf * TB, d);
+            // The first columns' scales, and whether all products of scales are normal
+            // numbers, while tensor memory answers.
+            constexpr int kHead = TB < 32 ? TB : 32;
+            float s[kHead];
+#pragma unroll
+            for (int j = 0; j < kHead; ++j) {
+                s[j] = sc[j] * sw;
+                asm volatile("" : "+f"(s[j]));  // (here, not behind the branch)
+            }
+            const float mine = sc[lane % TB] * sw, later = TB > 32 ? sc[lane + TB - 32] * sw : mine;
+            const bool plain = __all_sync(0xffffffffu, (in_range(mine) | no_token) & (in_range(later) | no_later));
+            tmem_wait_ld(d);
             if (plain) {
 #pragma unroll
                 for (int c = 0; c < TB; c += 16) {
-                    uint32_t d[16];
-                    tmem_ld16(lanes + buf * TB + c, d);
-                    tmem_wait_ld(d);
+                    if (c > 0) {
+                        tmem_ld16(lanes + buf * TB + c, d);
+                        tmem_wait_ld(d);
+                    }
 #pragma unroll
                     for (int j = 0; j < 16; ++j)
-                        acc[c + j] = fmaf(__uint_as_float(d[j]), sc[c + j] * sw, acc[c + j]);
+                        acc[c + j] = fmaf(__uint_as_float(d[j]), c < kHead ? s[c % kHead + j] : sc[c + j] * sw, acc[c + j]);
                 }
             } else {  // lane t splits the scales of tokens t and t + 32
                 const ScalePair own = split_scales(sc[lane % TB], sw), own32 = split_scales(sc[(lane + 32) % TB], sw);
 #pragma unroll
                 for (int c = 0; c < TB; c += 16) {
-                    uint32_t d[16];
                     tmem_ld16(lanes + buf * TB + c, d);
                     tmem_wait_ld(d);
 #pragma unroll
