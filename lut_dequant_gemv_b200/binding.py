@@ -464,6 +464,17 @@ def _raw_stream(stream, device: int) -> Optional[int]:
     return _stream(stream)
 
 
+def _empty(shape, dtype: torch.dtype, device: torch.device, stream) -> torch.Tensor:
+    """Memory that a call on `stream` writes: it belongs to that stream (what the current stream has freed may still
+    be in use there)."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _pitch(t: torch.Tensor, name: str) -> int:
     """Elements from one row to the next of a tensor whose rows are contiguous and, beyond two
     dimensions, evenly spaced; for a single row, its length rounded up to 16."""
@@ -491,8 +502,8 @@ def sqz_fp8_quantize(x: torch.Tensor, block_rows: int = 1, dtype: torch.dtype = 
                      q: Optional[torch.Tensor] = None, scale: Optional[torch.Tensor] = None, stream=None):
     """Quantize fp16/bf16 x [rows, cols] or [batch, rows, cols] (CUDA) to 8-bit codes with one fp32 scale per block of
     block_rows (1 or 128) x 128; returns (q, scale).  q has x's shape and an fp8 dtype on a 16-byte row pitch;
-    scale is [(batch,) ceil(rows / block_rows), ceil(cols / 128)].  Both are allocated unless given (q's dtype
-    then names the format)."""
+    scale is [(batch,) ceil(rows / block_rows), ceil(cols / 128)].  Both are allocated (on `stream`) unless given (q's
+    dtype then names the format)."""
     shape, dev = x.shape, _on_current_device(x, "x")
     if len(shape) not in (2, 3):
         raise ValueError("x must be [rows, cols] or [batch, rows, cols]")
@@ -504,12 +515,12 @@ def sqz_fp8_quantize(x: torch.Tensor, block_rows: int = 1, dtype: torch.dtype = 
     if q is None:
         if dtype not in _FP8_FORMATS:
             raise TypeError(f"dtype {dtype} is not an 8-bit floating-point type")
-        q = torch.empty((*shape[:-1], (cols + 15) // 16 * 16), dtype=dtype, device=x.device)[..., :cols]
+        q = _empty((*shape[:-1], (cols + 15) // 16 * 16), dtype, x.device, stream)[..., :cols]
     elif q.get_device() != dev or q.dtype not in _FP8_FORMATS or q.shape != shape:
         raise ValueError(f"q must have shape {tuple(shape)} and an fp8 dtype, on x's device")
     s_shape = (*shape[:-2], -(-rows // block_rows), -(-cols // 128))
     if scale is None:
-        scale = torch.empty(s_shape, dtype=torch.float32, device=x.device)
+        scale = _empty(s_shape, torch.float32, x.device, stream)
     elif scale.get_device() != dev or scale.dtype is not torch.float32 or scale.shape != s_shape:
         raise ValueError(f"scale must be fp32 of shape {s_shape}, on x's device")
     if rows and cols and (len(shape) == 2 or shape[0]):

@@ -173,3 +173,24 @@ def test_a_decoding_step(B, tokens):
         graph.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(want, (h, mixed, y)))
+
+
+@pytest.mark.parametrize("raw", [False, True])
+def test_outputs_made_for_another_stream(B, raw):
+    """q and scales that the call allocates belong to the stream it is given: memory that was freed on the current
+    stream may still be written there."""
+    x = torch.randn((300, 1024), generator=torch.Generator().manual_seed(4)).half().cuda()
+    want_q, want_s = B.sqz_fp8_quantize(x)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for _ in range(3):
+        torch.cuda.empty_cache()
+        busy = [torch.empty(300 * 1024, dtype=torch.uint8, device="cuda"), torch.empty(300 * 8, device="cuda")]
+        torch.cuda._sleep(20_000_000)  # about 10 ms, then the current stream writes what it has freed
+        for t in busy:
+            t.fill_(7)
+        del t, busy
+        q, s = B.sqz_fp8_quantize(x, stream=side.cuda_stream if raw else side)
+        torch.cuda.synchronize()
+        assert torch.equal(q.view(torch.uint8), want_q.view(torch.uint8)) and torch.equal(s, want_s)
+        del q, s
