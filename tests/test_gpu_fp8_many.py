@@ -172,3 +172,14 @@ def test_offsets_beyond_32_bits(B):
         y = torch.empty((m + 1) * ldy, device="cuda").view(m + 1, ldy)[:m, :n]
         B.sqz_fp8_gemm(q, s, w_far, sw, y)
         check_product(y, q, s, w, sw)
+
+
+def test_few_rows_of_a_matrix_wider_than_a_grid(B):
+    """More blocks of 128 rows of W than a grid's second dimension has: the many-row kernel, with two rows of A."""
+    m, n, k = 2, 65535 * 128 + 1, 20
+    assert B.sqz_fp8_plan_query(m, n, k)["many_rows"] == 1 and B.sqz_fp8_plan_query(m, n - 1, k)["many_rows"] == 0
+    a, sa, w, sw = operands(44, m, n, k)
+    for cols in (n, n - 1):
+        y = torch.full((m, cols), float("nan"), device="cuda")
+        B.sqz_fp8_gemm(a, sa, w[:cols], sw[: -(-cols // 128)], y)
+        check_product(y, a, sa, w[:cols], sw[: -(-cols // 128)])
