@@ -374,9 +374,11 @@ SQZ_API int64_t sqz_encode_outliers(int64_t n_weights, double outlier_fraction);
 /* ------------------------------------- 8-bit floating point, block scales ---
  * Products whose operands are 8-bit floating-point codes with one fp32 scale
  * for each block of 128 columns (of K), for calls the LUT kernels do not
- * serve: more than SQZ_MAX_BATCH columns (prompts; sqz_debug_dequant followed
- * by sqz_fp8_quantize turns a layer's dense part into such a matrix) and
- * layers kept at 8 bits.
+ * serve: more than SQZ_MAX_BATCH columns (prompts) and layers kept at 8 bits.
+ * sqz_debug_dequant followed by sqz_fp8_quantize turns a layer's dense part Q into
+ * such a matrix, rounded once more to 8 bits; the outliers S are not in it, so a
+ * layer that has some needs their product added (or W quantized from the
+ * weights that it was made of).
  *
  * A matrix X [rows][k] is held as codes q [rows][ld] (row-major, bytes) and
  * scales [ceil(rows / block_rows)][ld_scale]: X(r,c) = scale(r / block_rows,
@@ -527,22 +529,24 @@ SQZ_API sqz_status sqz_moe_workspace_bytes(sqz_moe_t moe, int32_t tokens, int64_
  * any of y is written); otherwise nothing may overlap.
  *
  * workspace: device memory on a 256-byte boundary of at least
- * sqz_moe_workspace_bytes(moe, tokens) bytes, zeroed once before its first
- * use with this handle; each call leaves it ready for the next, of any number
- * of tokens that fits.  Calls that share a workspace must not overlap (the
+ * sqz_moe_workspace_bytes(moe, tokens) bytes, zeroed before its first use;
+ * each call leaves it ready for the next with the same handle, of any number of
+ * tokens that fits (before it goes to another handle it is zeroed again: the
+ * places of its counters are the handle's).  Calls that share a workspace must not overlap (the
  * same stream, or ordered by events); calls with workspaces of their own may.
  * The launch is cooperative, one CTA on every SM, and may be captured into a
  * graph (which then owns its workspace while it runs).
  *
  * Arithmetic: the codes' products are exact; x and h enter the tensor cores
  * as four 8-bit digits each, which represent x exactly (values below 2^-10 of
- * the largest of their block of 128 within 2^-29 of it) and h to 2^-19; sums are
- * in fp32; y is rounded once.  The logits are summed in fp64 and compared to
- * 48 bits, so near-equal ones keep their order; the softmax is in fp32.
- * Bitwise reproducible for the same batch; a token's row may differ in its last
- * bits beside other tokens, since the work is cut by the experts they reach
- * together.  A token whose x or h is not finite, or whose logits
- * hold a NaN or pass fp32's range, gets NaN; its ids stay in range.
+ * the largest of their block of 128 within 2^-29 of it, or of 2^-110 where it is
+ * less) and h to 2^-19; scales may have any magnitude; sums are in fp32; y is
+ * rounded once.  The logits are summed in fp64 and compared to 48 bits, so
+ * near-equal ones keep their order; the softmax is in fp32.  Bitwise reproducible
+ * for the same batch; a token's row may differ in its last bits beside other
+ * tokens, since the work is cut by the experts they reach together.  A token
+ * whose x or h is not finite, or whose logits hold a NaN or pass fp32's range,
+ * gets NaN; its ids stay in range.
  *
  * Errors: SQZ_ERR_INVALID_ARG (NULL, tokens outside [0, SQZ_MOE_MAX_TOKENS],
  * pitches below hidden, a small or misaligned workspace, another device);

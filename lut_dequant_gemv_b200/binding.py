@@ -653,7 +653,8 @@ def sqz_moe_workspace_bytes(moe: Moe, tokens: int) -> int:
 
 
 def sqz_moe_workspace(moe: Moe, tokens: int) -> torch.Tensor:
-    """A zeroed workspace for calls of up to `tokens` tokens, on the current device."""
+    """A workspace for calls of up to `tokens` tokens with this handle, on the current device, zeroed on the current
+    stream."""
     return torch.zeros(sqz_moe_workspace_bytes(moe, tokens), dtype=torch.uint8, device="cuda")
 
 

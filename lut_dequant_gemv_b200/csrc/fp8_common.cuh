@@ -24,7 +24,6 @@ namespace f8 {
 using tc::cp_async_commit;
 using tc::cp_async_wait;
 using tc::fence_mbar_init;
-using tc::fence_proxy_async;
 using tc::mbar_arrive;
 using tc::mbar_expect_tx;
 using tc::mbar_init;

@@ -26,10 +26,12 @@ namespace f8 {
 // on keep it exact; blocks whose scale is outside [2^-80, 2^120] (or NaN, or
 // infinite) divide.
 //
-// Measured: 4096 x 13824 bf16 in 1 x 128 blocks 32.5 us, 5.3 TB/s (0.81 of the
-// copy rate), 11000 x 4100 fp16 in 128 x 128 blocks 30 us, 4.5 TB/s, a row of
-// 4096 1.6 us.  Bound by instructions (75 % of the issue slots, 15 an element),
-// half of them the quotients' and the maxima's.
+// Measured: 4096 x 13824 bf16 in 1 x 128 blocks 32.4 us, 5.3 TB/s (0.81 of the
+// copy rate), bound by instructions (75 % of the issue slots, 15 an element,
+// half of them the quotients' and the maxima's); 11000 x 4100 fp16 in 128 x 128
+// blocks 30 us, 4.5 TB/s, with 62 % of the issue slots: a CTA's loads, barrier and
+// stores follow one another, and the other three of its SM fill the gaps only in
+// part; a row of 4096 1.6 us.
 struct Quotient {
     float scale, inv;
     __device__ __forceinline__ explicit Quotient(float s) : scale(s), inv(1.f / s) {}
@@ -303,7 +305,7 @@ constexpr int kMaxStages = 12;
 //
 // Measured: 16 x 5120 x 13824 16.0 us, 4.4 TB/s with about 4 us of launch,
 // first copies and the sums' meeting (16 x 18944 x 32768: 6.1 TB/s); 1 x 4096 x
-// 4096 6.1 us.
+// 4096 6.1 us; 32 x 5120 x 5120 9.4; 64 x 5120 x 13824 19.9.
 //
 //   warp 0: TMA loads of W and A tiles into a ring of stages
 //   warp 1: TMEM allocation, matrix instructions into a ring of accumulators
@@ -474,7 +476,7 @@ __global__ void __launch_bounds__(224) fp8_gemm_few_kernel(const __grid_constant
             if (++st == p.stages) st = 0, ph ^= 1;
         }
     }
-    __syncwarp();  // one lane ran the role: the barrier counts whole warps
+    __syncwarp();  // a warp whose lanes parted in its role meets again: the barrier counts whole warps
     __syncthreads();
     tc_fence_after();
     if (warp == 1) tmem_dealloc(taddr, S::kTmemCols);
@@ -531,18 +533,23 @@ __global__ void __launch_bounds__(224) fp8_gemm_few_kernel(const __grid_constant
 // the 128-row blocks of W that its columns lie in).  Packed fp32 multiply-adds
 // measured slower here than plain ones.
 //
-// What bounds it: the two accumulators of 256 columns fill tensor memory, so
-// an accumulator's whole way -- the matrix instructions (512 cycles, up to 950
-// while the promotion reads tensor memory), their completion's arrival (200),
-// the promotion's reads (480), the arrival that frees it (210) and the issue
-// (200) -- is paid once for every two blocks: 1080 cycles a block, 8192 x 11008
-// x 4096 in 357 us (2.07 PFLOP/s, tensor pipe 49 %; 420 us under the power cap).
+// What bounds it, by the clocks of a CTA's roles (cycles a block of K):
+//   64 columns, eight accumulators: 495, of which the issuing warp spends 340 on
+//   the instructions of the block (four products, two commits, the next polls) and
+//   155 waiting.  The matrix instructions themselves take 128: the issue is what
+//   every width pays, and most of the 180 ns that a block costs at any width.
+//   256 columns, two accumulators: 935, of which the issue takes 335, a wait for
+//   an accumulator 485 and one for a stage 110.  The promotion has 935 as well:
+//   487 of reads, 248 of the last multiply-adds and its loop, 198 of waiting: an
+//   accumulator's way through it is what the issue waits for.
+// 8192 x 11008 x 4096 in 356 to 363 us (2.05 PFLOP/s, tensor pipe 47 %; 422 us
+// under the power cap, 1.75).
 //
 //   warp 0: TMA ring (the full barriers live in the even CTA, the empty ones
 //   in both), warp 1: TMEM and, in the even CTA, matrix instructions, warp 2:
 //   scales, sixteen blocks of K ahead (a wait for each block's would cost the
 //   promotion 200 cycles; loads into its registers stall its reads of tensor
-//   memory), warps 3-10: promotion (warp % 4 = the 32 lanes it may read; first
+//   memory), and whether their products stay in range, warps 3-10: promotion (warp % 4 = the 32 lanes it may read; first
 //   or second half of the columns)
 template <int BN>
 struct ManyShape {
@@ -895,7 +902,7 @@ __global__ void __launch_bounds__(ManyShape<BN>::kThreads, 1) fp8_gemm_many_kern
                 if (!odd_s[runs & 1]) {
 #pragma unroll 1
                     for (int kb = 0; kb < len && alive; ++kb) promote(sc, kb, std::false_type());
-                } else {  // (a loop of its own: tests in the other one cost it 3 to 30 %)
+                } else {  // (a loop of its own: a test of each block in the other one costs it 3 to 30 %)
 #pragma unroll 1
                     for (int kb = 0; kb < len && alive; ++kb) promote(sc, kb, std::true_type());
                 }
@@ -910,7 +917,7 @@ __global__ void __launch_bounds__(ManyShape<BN>::kThreads, 1) fp8_gemm_many_kern
             }
         }
     }
-    __syncwarp();  // one lane ran the role: the barrier counts whole warps
+    __syncwarp();  // a warp whose lanes parted in its role meets again: the barrier counts whole warps
     __syncthreads();
     cluster_sync();  // nothing of the other CTA is on its way here any more
     tc_fence_after();

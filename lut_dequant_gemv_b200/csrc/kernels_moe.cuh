@@ -18,12 +18,14 @@
 // digit is the rounded remainder of the ones before it, 16 times larger, so
 // four digits carry 19 bits of a block's large values (fp16 has 11, bf16 8:
 // both exact) and an absolute error of 2^-29 of the block's largest for small
-// ones.  A token is then four columns of the product, weights take the 128
+// ones.  (Blocks whose largest is below 2^-110 are scaled as if it were that.)  A
+// token is then four columns of the product, weights take the 128
 // lanes (the MMA's M), and the digits' columns are joined in fp32 when the
 // block's sum is scaled.
 //
 // Work.  A persistent CTA per SM; three phases with two grid-wide barriers:
-//   0  router logits and the digits of x, spread over all warps of the grid;
+//   0  router logits (in fp64: they are compared) and the digits of x, spread over
+//      all warps of the grid;
 //   1  every CTA routes for itself (the logits are a few KB), then gate and
 //      up products: units (expert, 128 columns of the inner size, block of K)
 //      in one sequence cut evenly over the CTAs, so that no SM is left with a
@@ -39,9 +41,10 @@
 // tiles of phase 2 are on their way while the CTA waits for the last h.
 //
 // Measured: 8 tokens, 128 experts, top 8, 4096/1408: 159 us for 894 MB (5.6
-// TB/s; 6.3 in phase 1); one token, 8 experts, top 2, 4096/11008: 66 us (4.1
-// TB/s); one token, 64 experts, top 6, 2048/1408: 34 us, of which the weights'
-// time is 8.  The rest is latency, and most of that is instructions that are not
+// TB/s; 6.3 in phase 1; 163 to 172 us where the weights come to lie elsewhere);
+// one token, 8 experts, top 2, 4096/11008: 66 us (4.1 TB/s); 32 tokens, 32
+// experts, top 4, 2560/1008: 77 us; one token, 64 experts, top 6, 2048/1408: 34
+// us, of which the weights' time is 8.  The rest is latency, and most of that is instructions that are not
 // in the cache the one time they run: routing 3.5 us after the first barrier, a
 // tile's end 5 us (the counter's round trip 1.5, the join 1.5 to 3, h and its
 // digits 0.5 to 3).  Code on those paths is kept short: unrolling the digits'
@@ -990,7 +993,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
             u += len;
         }
     }
-    __syncwarp();  // one lane ran the role: the barrier counts whole warps
+    __syncwarp();  // a warp whose lanes parted in its role meets again: the barrier counts whole warps
     __syncthreads();
     tc_fence_after();
     if (warp == 1) tmem_dealloc(taddr, 512);

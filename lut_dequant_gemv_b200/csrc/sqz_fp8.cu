@@ -172,8 +172,8 @@ Plan plan_product(int32_t m, int32_t n, int32_t k, int sms) {
     if (splits < 1) splits = 1;
     // Beyond 64 rows the few-row kernel serves products with so little W that the
     // many-row kernel's pairs would stand idle (it does not split K): a CTA's block
-    // of K takes about 400 ns (100 x 300 x 13824: 39 us, 11 this way; 128 x 4096 x
-    // 4096: 13.1 and 11.5).
+    // of K takes about 400 ns (100 x 300 x 13824: 39 us, 12 this way; 128 x 4096 x
+    // 4096: 13.1 and 11.9).
     const int64_t few = 5000 + (blocks * splits + sms - 1) / sms * ((nkb + splits - 1) / splits) * 400;
     if ((m <= kFewRows || few < many) && row_blocks <= 65535) return {false, 128, tb, splits};
     return {true, bn, 256, 1};
