@@ -353,7 +353,7 @@ __device__ __forceinline__ ScalePair split_scales(float a, float b) {
     const bool swap = fabsf(a) > fabsf(b);
     const float lo = swap ? b : a, hi = swap ? a : b;
     ScalePair r = {p, 1.f};
-    if (in_range(p) || lo == 0.f || !(fabsf(hi) < inf)) return r;  // zeros, infinities and NaN: as they are
+    if (in_range(p) || lo == 0.f || p != p || fabsf(hi) == inf) return r;  // zeros, infinities and NaN: as they are
     if (fabsf(p) < 1.f) {  // |lo| < 2^-63
         r.first = 0x1p-64f;
         r.s = lo * 0x1p64f * hi;

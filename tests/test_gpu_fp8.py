@@ -495,3 +495,27 @@ def test_quantize_at_every_alignment_of_the_rows(B, block_rows, dtype, fmt):
             q, s = B.sqz_fp8_quantize(x, block_rows, fmt)
             q_ref, s_ref = quantize_ref(big[off:].view(131, ldx)[:, :cols][None], block_rows, fmt)
             assert torch.equal(s.cpu(), s_ref[0]) and same_codes(q.cpu(), q_ref[0]), (cols, off, ldx)
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), float("-inf")])
+@pytest.mark.parametrize("m,n,k", SCALE_SHAPES)
+def test_product_with_one_scale_that_is_not_finite(B, m, n, k, value):
+    """Finite codes under a scale that is NaN or infinite, in A and in W, next to scales of every size: NaN, or infinite
+    (NaN where a block's sum is zero), in the outputs it enters, and the others as they are."""
+    gen = torch.Generator().manual_seed(23)
+    a, sa = random_matrix(gen, m, k, E4M3, 1)
+    w, sw = random_matrix(gen, n, k, E4M3, 128)
+    for big in (0, 60):  # products in range, and some that are not
+        A, W = sa.clone(), sw.clone()
+        A[0] *= 2.0 ** -big
+        W[0] *= 2.0 ** -big
+        A[2, 3], W[1, 4] = value, value
+        y = torch.empty((m, n), device="cuda")
+        B.sqz_fp8_gemm(a, A, w, W, y)
+        hit = torch.zeros((m, n), dtype=torch.bool, device="cuda")
+        hit[2], hit[:, 128:256] = True, True
+        if value != value:
+            assert bool(y[hit].isnan().all())
+        else:
+            assert not bool(y[hit].isfinite().any()) and bool(y[2, :128].isinf().any())
+        assert bool(y[~hit].isfinite().all())
