@@ -463,7 +463,8 @@ __global__ void __launch_bounds__(224) fp8_gemm_few_kernel(const __grid_constant
                     for (int j = 0; j < 16; ++j) {
                         const ScalePair& from = c + j < 32 ? own : own32;
                         const float f = __shfl_sync(0xffffffffu, from.first, (c + j) & 31);
-                        acc[c + j] = fmaf(__uint_as_float(d[j]) * f, __shfl_sync(0xffffffffu, from.s, (c + j) & 31), acc[c + j]);
+                        acc[c + j] =
+                            fmaf(__uint_as_float(d[j]) * f, __shfl_sync(0xffffffffu, from.s, (c + j) & 31), acc[c + j]);
                     }
                 }
             }
@@ -549,8 +550,8 @@ __global__ void __launch_bounds__(224) fp8_gemm_few_kernel(const __grid_constant
 //   in both), warp 1: TMEM and, in the even CTA, matrix instructions, warp 2:
 //   scales, sixteen blocks of K ahead (a wait for each block's would cost the
 //   promotion 200 cycles; loads into its registers stall its reads of tensor
-//   memory), and whether their products stay in range, warps 3-10: promotion (warp % 4 = the 32 lanes it may read; first
-//   or second half of the columns)
+//   memory), and whether their products stay in range, warps 3-10: promotion
+//   (warp % 4 = the 32 lanes it may read; first or second half of the columns)
 template <int BN>
 struct ManyShape {
     static constexpr int kRowsW = BN / 2;  // of W, in each CTA

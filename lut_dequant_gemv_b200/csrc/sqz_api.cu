@@ -1091,6 +1091,6 @@ void sqz_internal_set_last_error(const char* msg) { g_last_error = msg ? msg : "
 
 extern "C" {
 
-int32_t sqz_version(void) { return 400; }
+int32_t sqz_version(void) { return 401; }
 
 }  // extern "C"

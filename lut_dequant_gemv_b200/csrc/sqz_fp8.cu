@@ -334,7 +334,8 @@ extern "C" SQZ_API sqz_status sqz_fp8_status(void* stream, int32_t* status) {
                                               "synchronises, which a capture cannot contain");
     int device = 0;
     SQZ_F8_TRY(cudaGetDevice(&device), "cudaGetDevice");
-    if (device >= kMaxDevices) return host_fail(SQZ_ERR_UNSUPPORTED, "device %d: at most %d are told apart", device, kMaxDevices);
+    if (device >= kMaxDevices)
+        return host_fail(SQZ_ERR_UNSUPPORTED, "device %d: at most %d are told apart", device, kMaxDevices);
     uint32_t* count = nullptr;
     const sqz_status st = timeout_count(&count);
     if (st != SQZ_OK) return st;
