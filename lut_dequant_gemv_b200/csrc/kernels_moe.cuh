@@ -41,9 +41,10 @@
 // tiles of phase 2 are on their way while the CTA waits for the last h.
 //
 // Measured: 8 tokens, 128 experts, top 8, 4096/1408: 153 to 172 us for the 48 to
-// 56 experts that random tokens reach (5.6 TB/s; 6.3 in phase 1); one token, 8 experts, top 2, 4096/11008: 66 us (4.1 TB/s); 32 tokens, 32
-// experts, top 4, 2560/1008: 77 us; one token, 64 experts, top 6, 2048/1408: 34
-// us, of which the weights' time is 8.  The rest is latency, and most of that is instructions that are not
+// 56 experts that random tokens reach (5.6 TB/s; 6.3 in phase 1); one token, 8
+// experts, top 2, 4096/11008: 66 us (4.1 TB/s); 32 tokens, 32 experts, top 4,
+// 2560/1008: 77 us; one token, 64 experts, top 6, 2048/1408: 34 us, of which the
+// weights' time is 8.  The rest is latency, and most of that is instructions not
 // in the cache the one time they run: routing 3.5 us after the first barrier, a
 // tile's end 5 us (the counter's round trip 1.5, the join 1.5 to 3, h and its
 // digits 0.5 to 3).  Code on those paths is kept short: unrolling the digits'
